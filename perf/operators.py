@@ -251,9 +251,14 @@ def _v_order(x, D):
     return x.movedim(-2, -4).flatten(-4)
 
 
+def _ks_order(x):
+    """Scale bytes [..., 16 t, D/32] of a tile's keys -> stored [g][hh][D/32]."""
+    return x.unflatten(-2, (2, 8)).movedim(-3, -2).flatten(-3)
+
+
 def _vs_order(x):
-    """Scale bytes [..., 16 t, D/32] of a tile's values -> stored [c][h][o][D/32]."""
-    return x.unflatten(-2, (2, 4, 2)).movedim(-3, -4).flatten(-4)
+    """Scale bytes [..., 16 t, D/32] of a tile's values -> stored [c][D/32][h][o]."""
+    return x.unflatten(-2, (2, 4, 2)).movedim((-3, -1), (-4, -3)).flatten(-4)
 
 
 def _tile_bytes(k, v):
@@ -262,7 +267,7 @@ def _tile_bytes(k, v):
     (kc, ks), (vc, vs) = _quantize(k), _quantize(v)
     kc = kc[..., 0::2] | (kc[..., 1::2] << 4)  # channel 2p in the low four bits
     vc = vc[..., 0::2] | (vc[..., 1::2] << 4)
-    return torch.cat([_k_order(kc, D), _v_order(vc, D), ks.flatten(-2), _vs_order(vs)], -1)
+    return torch.cat([_k_order(kc, D), _v_order(vc, D), _ks_order(ks), _vs_order(vs)], -1)
 
 
 def _tile_values(tile):
@@ -278,9 +283,10 @@ def _tile_values(tile):
     v = tile[..., 8 * D:16 * D].unflatten(-1, (D // 64, 8, 4, 16)).movedim(-4, -2).flatten(-2)
     v = v.unflatten(-1, (2, 2, D // 32, 2)).movedim((-6, -5), (-2, -5))  # -> h c o b g j
     v = pairs(v.flatten(-3).flatten(-4, -2))
-    ks = tile[..., 16 * D:16 * D + D // 2].unflatten(-1, (16, D // 32))
-    vs = tile[..., 16 * D + D // 2:].unflatten(-1, (4, 2, 2, D // 32)).movedim(-4, -3)
-    return _values(k, ks), _values(v, vs.flatten(-4, -2))
+    ks = tile[..., 16 * D:16 * D + D // 2].unflatten(-1, (8, 2, D // 32)).movedim(-2, -3)
+    vs = tile[..., 16 * D + D // 2:].unflatten(-1, (4, D // 32, 2, 2))  # c b h o
+    vs = vs.movedim((-2, -4), (-4, -3)).movedim(-2, -1)                # -> h c o b
+    return _values(k, ks.flatten(-3, -2)), _values(v, vs.flatten(-4, -2))
 
 
 # ------------------------------------------------------------------------- plain forms ----
@@ -334,7 +340,9 @@ def _plain_rows(s):
     inv[_v_order(at.view(16, D // 2), D)] = at
     v_at = inv.view(16, D // 2) + 8 * D
     at = torch.arange(D // 2, device=k.device)
-    ks_at = at.view(16, D // 32) + 16 * D
+    inv = torch.empty_like(at)
+    inv[_ks_order(at.view(16, D // 32))] = at
+    ks_at = inv.view(16, D // 32) + 16 * D
     inv = torch.empty_like(at)
     inv[_vs_order(at.view(16, D // 32))] = at
     vs_at = inv.view(16, D // 32) + 16 * D + D // 2
@@ -452,8 +460,8 @@ def _exact_tiles(tiles):
     lane = ((d % 32) // 4) * 4 + (t % 8) // 2
     v_in = (2 * (t // 8) + t % 2) * (D // 16) + 2 * (d // 32) + (d % 4) // 2
     v_byte = 8 * D + (v_in // 16) * 512 + lane * 16 + v_in % 16
-    ks = 16 * D + t * (D // 32) + d // 32
-    vs = 16 * D + D // 2 + (((t % 8) // 2) * 4 + (t // 8) * 2 + t % 2) * (D // 32) + d // 32
+    ks = 16 * D + t % 8 * (D // 16) + t // 8 * (D // 32) + d // 32
+    vs = 16 * D + D // 2 + (t % 8) // 2 * (D // 8) + d // 32 * 4 + t // 8 * 2 + t % 2
     up = 4 * (d % 2)
     return (_exact_code_values((tiles[:, k_byte] >> up) & 15, tiles[:, ks]),
             _exact_code_values((tiles[:, v_byte] >> up) & 15, tiles[:, vs]))
