@@ -214,10 +214,10 @@ def prepare(case, seed):
 
 def _quantize(x):
     """bf16 [..., D] -> E2M1 codes [..., D] and E8M0 scale bytes [..., D / 32] (both uint8):
-    the scale is the smallest power of two (2^-126 at least) with |x| <= 6 times it."""
+    the scale is the smallest power of two with |x| <= 6 times it, from 2^-126 to 2^125."""
     b = x.float().unflatten(-1, (x.shape[-1] // 32, 32))
     m, e = torch.frexp(b.abs().amax(-1))  # amax = m 2^e, m in [0.5, 1)
-    e = (e - 3 + (m > 0.75).int()).clamp(min=-126)
+    e = (e - 3 + (m > 0.75).int()).clamp(-126, 125)
     e = torch.where(m == 0, torch.full_like(e, -126), e)
     y = torch.ldexp(b, -e[..., None])
     a = y.abs()
@@ -474,7 +474,7 @@ def _exact_rows(x):
     amax = b.abs().amax(-1, keepdim=True)
     e = torch.ceil(torch.log2((amax / 6).clamp(min=2.0 ** -126)))
     e = torch.where(6 * torch.exp2(e - 1) >= amax, e - 1, e)  # log2 near a whole number
-    e = torch.where(6 * torch.exp2(e) < amax, e + 1, e).clamp(min=-126)
+    e = torch.where(6 * torch.exp2(e) < amax, e + 1, e).clamp(-126, 125)
     y = b / torch.exp2(e)
     hi = torch.searchsorted(grid, y.abs().contiguous()).clamp(max=7)
     lo = (hi - 1).clamp(min=0)
