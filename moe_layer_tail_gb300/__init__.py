@@ -12,6 +12,11 @@ the binding raises: there is no CPU or PyTorch fallback.
 import ctypes
 import os
 
+from . import kv4
+from .kv4 import (KV4_STATUS_BAD_LENGTH, KV4_STATUS_BAD_PAGE, KV4_STATUS_BAD_SLOT,
+                  KV4_STATUS_NO_PAGES, KV4_STATUS_ROWS, kv4_append, kv4_attention,
+                  kv4_attention_workspace, kv4_cache, kv4_read, qk_norm_rope, step_tables)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmoe_tail.so")
 
@@ -133,6 +138,7 @@ def load_library(path: str = None):
     lib.moe_attnres_mix_get_status.restype = ctypes.c_int
     lib.moe_attnres_mix_ctas_per_row.argtypes = [i32, i32]
     lib.moe_attnres_mix_ctas_per_row.restype = ctypes.c_int
+    kv4.declare(lib)
     _lib = lib
     return lib
 

@@ -15,6 +15,8 @@
 #include <math.h>
 
 #include "attnres_mix.h"
+#include "kv4_attn.h"
+#include "k_kv4.cuh"
 #include "k_mix.cuh"
 #include "k_persist.cuh"
 #include "moe_tail.h"
@@ -699,6 +701,217 @@ extern "C" int moe_attnres_mix_get_status(int* status, int clear) {
   if (e != cudaSuccess) return cuda_fail(e);
   *status = v;
   return v ? MOE_TAIL_ERR_DEVICE : MOE_TAIL_OK;
+}
+
+// -------------------------------------- the decode step's attention block (kv4_attn.h) ----
+
+namespace {
+
+bool row_stride_ok(int64_t ld, int64_t width) { return ld >= width && ld % 8 == 0; }
+bool page_ok(int32_t page) { return page >= 16 && page <= kv4::kMaxPage && page % 16 == 0; }
+bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
+
+int kv4_rows(bool append, int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+             int64_t n_pages, const void* cache, const void* k, int64_t ld_k, const void* v,
+             int64_t ld_v, const int64_t* slots, int32_t* status, void* stream) {
+  if (rows < 1 || rows > kv4::kMaxRows || n_pages < 1 || n_pages > INT32_MAX)
+    return MOE_TAIL_ERR_INVALID_ARG;
+  if (kv_heads < 1 || kv_heads > kv4::kMaxKvHeads || !head_dim_ok(head_dim) || !page_ok(page_size))
+    return MOE_TAIL_ERR_UNSUPPORTED;
+  if (!cache || !k || !v || !slots || !aligned16(cache) || !aligned16(k) || !aligned16(v))
+    return MOE_TAIL_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)kv_heads * head_dim;
+  if (!row_stride_ok(ld_k, width) || !row_stride_ok(ld_v, width)) return MOE_TAIL_ERR_INVALID_ARG;
+  kv4::RowsArgs a;
+  a.rows = rows;
+  a.heads = kv_heads;
+  a.D = head_dim;
+  a.page = page_size;
+  a.n_slots = n_pages * page_size;
+  a.cache = (uint8_t*)cache;
+  a.k = (uint16_t*)k;
+  a.v = (uint16_t*)v;
+  a.ldk = ld_k;
+  a.ldv = ld_v;
+  a.slots = slots;
+  a.status = status;
+  const cudaError_t e = append ? kv4::launch_kv4_append(a, (cudaStream_t)stream)
+                               : kv4::launch_kv4_read(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_TAIL_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" int moe_step_tables(int32_t reqs, int32_t max_rows, int32_t page_size, int32_t n_free,
+                               int32_t table_width, int64_t table_stride,
+                               const int32_t* cached_lens, const int32_t* new_lens,
+                               const int32_t* free_pages, int32_t* block_table,
+                               int32_t* row_starts, int32_t* kv_lens, int32_t* positions,
+                               int64_t* slots, int32_t* pages_used, int32_t* status,
+                               void* stream) {
+  if (reqs < 1 || max_rows < 1 || n_free < 0 || table_width < 1 || table_stride < table_width)
+    return MOE_TAIL_ERR_INVALID_ARG;
+  if (reqs > kv4::kMaxReqs || max_rows > kv4::kMaxRows || !page_ok(page_size))
+    return MOE_TAIL_ERR_UNSUPPORTED;
+  if (!cached_lens || !new_lens || (n_free > 0 && !free_pages) || !block_table || !row_starts ||
+      !kv_lens || !positions || !slots || !pages_used)
+    return MOE_TAIL_ERR_INVALID_ARG;
+  if (kv_lens == cached_lens || kv_lens == new_lens) return MOE_TAIL_ERR_INVALID_ARG;
+  kv4::TablesArgs a;
+  a.reqs = reqs;
+  a.max_rows = max_rows;
+  a.page = page_size;
+  a.n_free = n_free;
+  a.width = table_width;
+  a.stride = table_stride;
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.free_pages = free_pages;
+  a.table = block_table;
+  a.row_starts = row_starts;
+  a.kv_lens = kv_lens;
+  a.positions = positions;
+  a.slots = slots;
+  a.used = pages_used;
+  a.status = status;
+  const cudaError_t e = kv4::launch_step_tables(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_TAIL_OK : cuda_fail(e);
+}
+
+extern "C" int moe_qk_norm_rope(int32_t rows, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                                int32_t rot_dim, int32_t interleaved, float eps, const void* q,
+                                int64_t ld_q, const void* k, int64_t ld_k, const void* q_gamma,
+                                const void* k_gamma, const int32_t* positions,
+                                const float* inv_freq, void* q_out, int64_t ld_qo, void* k_out,
+                                int64_t ld_ko, void* stream) {
+  if (rows < 1 || rows > kv4::kMaxRows || !(eps > 0.f) || !isfinite(eps))
+    return MOE_TAIL_ERR_INVALID_ARG;
+  if (q_heads < 1 || q_heads > 1024 || k_heads < 0 || k_heads > 1024 || head_dim < 16 ||
+      head_dim > 256 || head_dim % 16 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
+    return MOE_TAIL_ERR_UNSUPPORTED;
+  const void* need[] = {q, q_out, k_heads ? k : q, k_heads ? k_out : q_out};
+  for (const void* p : need)
+    if (!p || !aligned16(p)) return MOE_TAIL_ERR_INVALID_ARG;
+  if ((q_gamma && !aligned16(q_gamma)) || (k_heads && k_gamma && !aligned16(k_gamma)) ||
+      (rot_dim > 0 && (!positions || !inv_freq)))
+    return MOE_TAIL_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)q_heads * head_dim, wk = (int64_t)k_heads * head_dim;
+  if (!row_stride_ok(ld_q, wq) || !row_stride_ok(ld_qo, wq) ||
+      (k_heads && (!row_stride_ok(ld_k, wk) || !row_stride_ok(ld_ko, wk))) ||
+      (q == q_out && ld_q != ld_qo) || (k_heads && k == k_out && ld_k != ld_ko))
+    return MOE_TAIL_ERR_INVALID_ARG;
+  kv4::RopeArgs a;
+  a.rows = rows;
+  a.hq = q_heads;
+  a.hk = k_heads;
+  a.D = head_dim;
+  a.rot = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.eps = eps;
+  a.q = (const uint16_t*)q;
+  a.k = (const uint16_t*)k;
+  a.qo = (uint16_t*)q_out;
+  a.ko = (uint16_t*)k_out;
+  a.ldq = ld_q;
+  a.ldk = ld_k;
+  a.ldqo = ld_qo;
+  a.ldko = ld_ko;
+  a.gq = (const uint16_t*)q_gamma;
+  a.gk = (const uint16_t*)k_gamma;
+  a.pos = positions;
+  a.freq = inv_freq;
+  const cudaError_t e = kv4::launch_qk_norm_rope(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_TAIL_OK : cuda_fail(e);
+}
+
+extern "C" int moe_kv4_append(int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                              int64_t n_pages, void* cache, const void* k, int64_t ld_k,
+                              const void* v, int64_t ld_v, const int64_t* slots, int32_t* status,
+                              void* stream) {
+  return kv4_rows(true, rows, kv_heads, head_dim, page_size, n_pages, cache, k, ld_k, v, ld_v,
+                  slots, status, stream);
+}
+
+extern "C" int moe_kv4_read(int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                            int64_t n_pages, const void* cache, void* k, int64_t ld_k, void* v,
+                            int64_t ld_v, const int64_t* slots, int32_t* status, void* stream) {
+  return kv4_rows(false, rows, kv_heads, head_dim, page_size, n_pages, cache, k, ld_k, v, ld_v,
+                  slots, status, stream);
+}
+
+static bool kv4_heads_ok(int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  return kv_heads >= 1 && kv_heads <= kv4::kMaxKvHeads && head_dim_ok(head_dim) && q_heads >= 1 &&
+         q_heads % kv_heads == 0 && q_heads / kv_heads <= 256;
+}
+
+extern "C" int64_t moe_kv4_attention_workspace(int32_t q_heads, int32_t kv_heads,
+                                               int32_t head_dim, int32_t max_new) {
+  if (max_new < 1) return MOE_TAIL_ERR_INVALID_ARG;
+  if (!kv4_heads_ok(q_heads, kv_heads, head_dim)) return MOE_TAIL_ERR_UNSUPPORTED;
+  const int rn = kv4::attn_rows_per_item(head_dim, q_heads / kv_heads, max_new);
+  cudaError_t e = cudaSuccess;
+  const int ctas = kv4::attn_ctas(head_dim, rn, &e);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return (int64_t)kv4::attn_workspace_bytes(head_dim, rn, ctas);
+}
+
+extern "C" int moe_kv4_attention(int32_t rows, int32_t reqs, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, int32_t page_size, int64_t n_pages,
+                                 const void* q, int64_t ld_q, const void* cache,
+                                 const int32_t* block_table, int32_t table_width,
+                                 int64_t table_stride, const int32_t* row_starts,
+                                 const int32_t* kv_lens, float scale, int32_t window,
+                                 int32_t sinks, int32_t max_new, void* out, int64_t ld_o,
+                                 void* workspace, size_t workspace_bytes, int32_t* status,
+                                 void* stream) {
+  if (rows < 1 || reqs < 1 || n_pages < 1 || n_pages > INT32_MAX || table_width < 1 ||
+      table_stride < table_width || !(scale > 0.f) || !isfinite(scale) || window < 0 ||
+      sinks < 0 || max_new < 1)
+    return MOE_TAIL_ERR_INVALID_ARG;
+  if (rows > (1 << 20) || reqs > kv4::kMaxReqs || !kv4_heads_ok(q_heads, kv_heads, head_dim) ||
+      !page_ok(page_size))
+    return MOE_TAIL_ERR_UNSUPPORTED;
+  const void* need[] = {q, cache, out, workspace};
+  for (const void* p : need)
+    if (!p || !aligned16(p)) return MOE_TAIL_ERR_INVALID_ARG;
+  if (!block_table || !row_starts || !kv_lens) return MOE_TAIL_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)q_heads * head_dim;
+  if (!row_stride_ok(ld_q, wq) || !row_stride_ok(ld_o, wq)) return MOE_TAIL_ERR_INVALID_ARG;
+  kv4::AttnArgs a;
+  a.G = q_heads / kv_heads;
+  a.D = head_dim;
+  const int rn = kv4::attn_rows_per_item(head_dim, a.G, max_new);
+  cudaError_t e = cudaSuccess;
+  a.ctas = kv4::attn_ctas(head_dim, rn, &e);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (workspace_bytes < kv4::attn_workspace_bytes(head_dim, rn, a.ctas))
+    return MOE_TAIL_ERR_INVALID_ARG;
+  a.q = (const uint16_t*)q;
+  a.ldq = ld_q;
+  a.cache = (const uint8_t*)cache;
+  a.n_pages = n_pages;
+  a.rows = rows;
+  a.reqs = reqs;
+  a.heads = kv_heads;
+  a.page_tiles = page_size / 16;
+  // tile / page_tiles = tile * magic >> 34 for tile < 2^27, page_tiles <= 64: the magic's excess
+  // over 2^34 / page_tiles is below 1, its product with the tile below 2^27 < 2^34 / page_tiles
+  a.page_magic = ((1ull << 34) + a.page_tiles - 1) / a.page_tiles;
+  a.table = block_table;
+  a.stride = table_stride;
+  const int64_t held = (int64_t)table_width * page_size;
+  a.max_len = (int)(held < INT32_MAX - 1024 ? held : INT32_MAX - 1024);
+  a.row_starts = row_starts;
+  a.kv_lens = kv_lens;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.window = window;
+  a.sinks = sinks;
+  a.out = (uint16_t*)out;
+  a.ldo = ld_o;
+  a.part = (float*)workspace;
+  a.status = status;
+  e = kv4::launch_kv4_attention(a, rn, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_TAIL_OK : cuda_fail(e);
 }
 
 extern "C" int moe_tail_check_scratch(moe_tail_t* h) {
