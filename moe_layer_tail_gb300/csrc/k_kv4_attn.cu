@@ -40,7 +40,7 @@ using mtail::bulk_load;
 using mtail::mbar_arrive;
 using mtail::mbar_expect_tx;
 using mtail::mbar_init;
-using mtail::mbar_wait;
+using mtail::mbar_try_wait;
 using mtail::mma_f16;
 using mtail::mma_f16_z;
 
@@ -49,9 +49,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMinTiles = 8;               // of a CTA's range
-constexpr uint64_t kBudgetNs = 100000000;  // of a wait for a tile
+constexpr int64_t kBudgetClocks = 200000000;  // of a wait for a tile, about 0.1 s
 constexpr float kLow = -3.0e38f;           // a row's reference before its first score
-constexpr int kUnset = -1000;              // a block's window before its first tile
 
 template <int D, int NT>
 struct Geo {
@@ -60,15 +59,16 @@ struct Geo {
   static constexpr int kTile = 17 * D;
   static constexpr int kStages = D == 256 ? 3 : 4;
   static constexpr int kQRow = 2 * D + 64;  // bytes: odd rows 64 bytes further, no conflicts
-  static constexpr bool kQReg = D * NT <= 256;
+  static constexpr bool kQReg = D * NT <= 128;
   static constexpr int kORegs = NB * 2 * NT * 4;
-  static constexpr int kBlocks = D == 256 ? 2 : (D == 128 && NT >= 2) ? (NT == 2 ? 3 : 2) : 4;
+  static constexpr int kBlocks = kORegs >= 128 ? 2 : kORegs >= 64 ? 3 : 4;  // CTAs per SM
   // shared memory: ring, two merge buffers, queries, then the small arrays
   static constexpr int kRing = kWarps * kStages * kTile;
   static constexpr int kMerge = 2 * kORegs * 32 * 4;
   static constexpr int kQ = RN * kQRow;
   static constexpr int kSmall = RN * 8 /* rowpos, qs */ + kWarps * RN * 8 /* m, l */ +
-                                kWarps * NB * 4 /* windows */ + kWarps * kStages * 8;
+                                kWarps * NB * 4 /* windows */ + kWarps * kStages * 8 +
+                                kWarps * 36 * 8 /* queues and walks */ + 64 /* notes */;
   static constexpr size_t smem(int reqs) {
     return (size_t)kRing + kMerge + kQ + kSmall + (size_t)(3 * reqs + 2) * 4;
   }
@@ -205,13 +205,27 @@ __device__ __forceinline__ uint32_t has_ff(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
 }
 
+// Bounded wait for a tile: false when the budget ran out.
+__device__ __forceinline__ bool tile_wait(uint64_t* b, uint32_t parity) {
+  if (mbar_try_wait(b, parity)) return true;
+  const int64_t t0 = clock64();
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(b, parity)) return true;
+  } while (clock64() - t0 < kBudgetClocks);
+  return false;
+}
+
 // What a warp keeps of the item it works on.
 template <int D, int NT>
 struct State {
   float o[D / 32][2][NT][4];  // [block][16 channels][8 rows]: channels 4 g + 2 mt + {0, 0, 1, 1}
                               // of the block, rows 8 nt + 2 c + {0, 1, 0, 1}
   float m[NT][2], l[NT][2];   // reference (less 11) and this lane's share of the sum
-  int lo[D / 32];             // o = sum * 2^(127 - 14 - lo)
+  uint32_t lo4[D / 32];       // window [lo, lo + 15] of the block's value scales, lo in each byte:
+                              // o = sum * 2^(127 - 14 - lo)
+  bool placed;                // the windows stand where the item's scales are
 };
 
 template <int D, int NT>
@@ -224,12 +238,12 @@ __device__ __forceinline__ void scale_block(State<D, NT>& st, int b, float f) {
       for (int e = 0; e < 4; ++e) st.o[b][mt][nt][e] *= f;
 }
 
-// One tile of 16 tokens in shared memory.  kMask: some of its (token, row) pairs are not seen.
-template <int D, int NT, bool kMask>
+// One tile of 16 tokens in shared memory.  partial: some of its (token, row) pairs are not seen.
+template <int D, int NT>
 __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, const uint8_t* sq,
                                           const uint32_t (&qr)[Geo<D, NT>::kQReg ? D / 32 : 1][NT][4],
-                                          const float (&qs)[NT][2], const int* rowpos, int t0,
-                                          int pmax, int window, int sinks) {
+                                          const float (&qs)[NT][2], const int* rowpos, bool partial,
+                                          int t0, int pmax, int window, int sinks) {
   constexpr int NB = D / 32;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   uint32_t kw[2 * NB], ks[NB / 2], vs[NB];
@@ -259,44 +273,61 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
       vs[4 * v] = u.x, vs[4 * v + 1] = u.y, vs[4 * v + 2] = u.z, vs[4 * v + 3] = u.w;
     }
   }
-  // a NaN scale, or a value scale outside its block's window [lo, lo + 15] (lo <= 239, so that
-  // 255 is always outside; a byte below lo borrows from the next one, but is itself outside)
-  uint32_t bad_k = 0, bad_v = 0;
-#pragma unroll
-  for (int i = 0; i < NB / 2; ++i) bad_k |= has_ff(ks[i]);
   // slots past the last row's position may hold anything: their value scales are put in the window
   uint32_t past = 0;
-  if constexpr (kMask) {
+  if (partial) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (t0 + 2 * c + (i & 1) + 8 * (i >> 1) > pmax) past |= 0xFFu << (8 * i);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      vs[b] = select_bits(past, vs[b], (uint32_t)max(st.lo[b], 0) * 0x01010101u);
+    for (int b = 0; b < NB; ++b) vs[b] = select_bits(past, vs[b], st.lo4[b]);
   }
+  // a NaN scale, or a value scale outside its block's window [lo, lo + 15] (lo <= 239, so that
+  // 255 is always outside; a byte below lo borrows from the next one, but is itself outside)
+  uint32_t bad = 0;
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    bad_v |= st.lo[b] < 0 ? ~0u : (vs[b] - (uint32_t)st.lo[b] * 0x01010101u) & 0xF0F0F0F0u;
+  for (int i = 0; i < NB / 2; ++i) bad |= has_ff(ks[i]);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) bad |= (vs[b] - st.lo4[b]) & 0xF0F0F0F0u;
+  bool nan_key = false, outside = false;
+  if (!st.placed || __any_sync(~0u, bad != 0)) {
+    bad = 0;
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) bad |= has_ff(ks[i]);
+    nan_key = __any_sync(~0u, bad != 0);
+    // place the windows anew: the first tile of an item, or scales far above all so far
+    bad = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      int hi = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int v = (int)(vs[b] >> (8 * i) & 255);
+        if (v != 255 && !(past >> (8 * i) & 1)) hi = max(hi, v);
+      }
+      hi = __reduce_max_sync(~0u, hi);
+      const int old = (int)(st.lo4[b] & 255);
+      if (!st.placed || hi > old + 15) {
+        const int lo = min(max(hi - 10, 0), 239);
+        if (st.placed) scale_block(st, b, exp2f((float)(old - lo)));
+        st.lo4[b] = (uint32_t)lo * 0x01010101u;
+      }
+      vs[b] = select_bits(past, vs[b], st.lo4[b]);
+      bad |= (vs[b] - st.lo4[b]) & 0xF0F0F0F0u;
+    }
+    st.placed = true;
+    outside = __any_sync(~0u, bad != 0);
+  }
 
   // ---- S^T = K Q^T
   float s[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-  const bool any_bad_k = __any_sync(~0u, bad_k != 0);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     uint32_t x[4], y[4];
     mtail::e2m1x8_to_f16x2(kw[b], x[0], x[1], x[2], x[3]);
     mtail::e2m1x8_to_f16x2(kw[NB + b], y[0], y[1], y[2], y[3]);
-    float f0 = mtail::e8m0_byte(ks[b / 4], b % 4);
-    float f1 = mtail::e8m0_byte(ks[(NB + b) / 4], (NB + b) % 4);
-    if (any_bad_k) {
-      const float nan = __uint_as_float(0x7FC00000u);
-      if (f0 == INFINITY) f0 = nan;
-      if (f1 == INFINITY) f1 = nan;
-    }
+    const float f0 = mtail::e8m0_byte(ks[b / 4], b % 4);
+    const float f1 = mtail::e8m0_byte(ks[(NB + b) / 4], (NB + b) % 4);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint32_t q0, q1, q2, q3;
@@ -310,16 +341,30 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
       float acc[4];
       mma_f16_z(acc, x[0], y[0], x[1], y[1], q0, q1);
       mma_f16(acc, x[2], y[2], x[3], y[3], q2, q3);
-      s[nt][0] = fmaf(acc[0], f0, s[nt][0]);
-      s[nt][1] = fmaf(acc[1], f0, s[nt][1]);
-      s[nt][2] = fmaf(acc[2], f1, s[nt][2]);
-      s[nt][3] = fmaf(acc[3], f1, s[nt][3]);
+      s[nt][0] = b ? fmaf(acc[0], f0, s[nt][0]) : acc[0] * f0;
+      s[nt][1] = b ? fmaf(acc[1], f0, s[nt][1]) : acc[1] * f0;
+      s[nt][2] = b ? fmaf(acc[2], f1, s[nt][2]) : acc[2] * f1;
+      s[nt][3] = b ? fmaf(acc[3], f1, s[nt][3]) : acc[3] * f1;
+    }
+  }
+  if (nan_key) {  // (the scale byte 255 came in as an infinity)
+    bool n0 = false, n1 = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      n0 = n0 || (ks[b / 4] >> (8 * (b % 4)) & 255) == 255;
+      n1 = n1 || (ks[(NB + b) / 4] >> (8 * ((NB + b) % 4)) & 255) == 255;
+    }
+    const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (n0) s[nt][0] = s[nt][1] = nan;
+      if (n1) s[nt][2] = s[nt][3] = nan;
     }
   }
 
   // ---- P^T = 2^(S - m)
   uint32_t hidden = 0;  // bit nt * 4 + e: the pair is masked
-  if constexpr (kMask) {
+  if (partial) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -335,7 +380,6 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[nt][e] = fmaf(s[nt][e], qs[nt][e & 1], -st.m[nt][e & 1]);
-      if (kMask && (hidden >> (nt * 4 + e) & 1)) x[nt][e] = -INFINITY;  // (q s = 0: NaN)
       top = fmaxf(top, x[nt][e]);
     }
   if (__any_sync(~0u, top > 14.f)) {  // 2^14 * 2^(15 + 1 - 15) stays below the f16 maximum
@@ -343,9 +387,7 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float y0 = s[nt][e] * qs[nt][e], y1 = s[nt][e + 2] * qs[nt][e];
-        if (kMask && (hidden >> (nt * 4 + e) & 1)) y0 = -INFINITY;
-        if (kMask && (hidden >> (nt * 4 + e + 2) & 1)) y1 = -INFINITY;
+        const float y0 = s[nt][e] * qs[nt][e], y1 = s[nt][e + 2] * qs[nt][e];
         float t = fmaxf(y0, y1);
         t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
         t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
@@ -373,37 +415,17 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
     for (int e = 0; e < 4; ++e) {
       p[e] = ex2(x[nt][e]);
       st.l[nt][e & 1] += p[e];
-      if (kMask && (hidden >> (nt * 4 + e) & 1)) p[e] = -0.f;  // marks a masked pair
+    }
+    if (partial) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (hidden >> (nt * 4 + e) & 1) p[e] = -0.f;  // marks a masked pair
     }
     pb[nt][0] = transpose8(pack_f16(p[0], p[1]));
     pb[nt][1] = transpose8(pack_f16(p[2], p[3]));
   }
 
   // ---- O^T += V^T P^T
-  if (__any_sync(~0u, bad_v != 0)) {
-    // place the windows anew: the first tile of an item, or scales far above all so far
-    bad_v = 0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      int hi = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int v = (int)(vs[b] >> (8 * i) & 255);
-        if (v != 255 && !(past >> (8 * i) & 1)) hi = max(hi, v);
-      }
-      hi = __reduce_max_sync(~0u, hi);
-      if (st.lo[b] < 0 || hi > st.lo[b] + 15) {
-        const int lo = min(max(hi - 10, 0), 239);
-        if (st.lo[b] >= 0) scale_block(st, b, exp2f((float)(st.lo[b] - lo)));
-        st.lo[b] = lo;
-      }
-      if (kMask) vs[b] = select_bits(past, vs[b], (uint32_t)st.lo[b] * 0x01010101u);
-      bad_v |= (vs[b] - (uint32_t)st.lo[b] * 0x01010101u) & 0xF0F0F0F0u;
-    }
-    bad_v = __any_sync(~0u, bad_v != 0);
-  } else {
-    bad_v = 0;
-  }
   uint32_t vw[D / 16];  // words of (h, o): [2 h + o][D / 64]
 #pragma unroll
   for (int v = 0; v < D / 64; ++v) {
@@ -424,9 +446,9 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
     for (int bb = 0; bb < 2; ++bb) {
       const int b = 2 * bp + bb, i = 2 * bb;
       const uint32_t s0 = __byte_perm(vs[b], 0, 0x4140), s1 = __byte_perm(vs[b], 0, 0x4342);
-      if (!bad_v) {
+      if (!outside) {
         // f16 with the exponent field s - lo + 1: 2^(s - lo - 14)
-        const uint32_t add = (uint32_t)(1 - st.lo[b]) * 0x04000400u;
+        const uint32_t add = 0x04000400u - (st.lo4[b] & 0x00FF00FFu) * 1024u;
         const uint32_t f0 = s0 * 1024u + add, f1 = s1 * 1024u + add;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -436,9 +458,10 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
         }
       } else {
         // window after window, from the largest scale down; NaN scales with the first
-        int sv[4] = {(int)(s0 & 255), (int)(s0 >> 16), (int)(s1 & 255), (int)(s1 >> 16)};
+        const int sv[4] = {(int)(s0 & 255), (int)(s0 >> 16), (int)(s1 & 255), (int)(s1 >> 16)};
         bool first = true;
         int below = 255;
+#pragma unroll 1
         for (int pass = 0; pass < 17; ++pass) {  // 255 / 16 windows at most
           int hi = -1;
 #pragma unroll
@@ -452,7 +475,7 @@ __device__ __forceinline__ void tile_step(State<D, NT>& st, const uint8_t* tp, c
           for (int k = 0; k < 4; ++k)
             f[k] = first && sv[k] == 255 ? 0x7E00u
                    : sv[k] < below && sv[k] >= lo ? (uint32_t)(sv[k] - lo + 1) << 10 : 0u;
-          const float back = exp2f((float)(lo - st.lo[b]));
+          const float back = exp2f((float)(lo - (int)(st.lo4[b] & 255)));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             uint32_t pp[2];
@@ -492,7 +515,9 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
   float* merge = reinterpret_cast<float*>(sm + G::kRing);
   uint8_t* sq = sm + G::kRing + G::kMerge;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sq + G::kQ);
-  int* rowpos = reinterpret_cast<int*>(bars + kWarps * G::kStages);
+  int64_t* queues = reinterpret_cast<int64_t*>(bars + kWarps * G::kStages);
+  int* notes = reinterpret_cast<int*>(queues + kWarps * 36);
+  int* rowpos = notes + 16;
   float* sqs = reinterpret_cast<float*>(rowpos + RN);
   float* xm = sqs + RN;                  // [warp][RN]
   float* xl = xm + kWarps * RN;          // [warp][RN]
@@ -523,62 +548,66 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
   }
   __syncwarp();
 
-  // ---- the copies of this warp's tiles, running ahead of the arithmetic by up to kStages tiles
-  struct {
-    Seg s;
-    uint32_t next;  // first tile of the range's next part
-    int i;          // next tile of the part
-    const int32_t* trow;
-    int tile, page; // the tile to copy next and its page (-1: none)
-    bool any;
-  } pr = {};
+  // ---- the copies of this warp's tiles, running ahead of the arithmetic by up to kStages tiles.
+  // A queue holds where the next (up to 32) tiles of the warp stand in the cache, one lane having
+  // looked up each; it is filled again, from the same or the range's next part, when it is empty.
+  // The walk itself (where its part begins in the range, the part's next tile of this warp or -1,
+  // the request) waits in shared memory: registers that the arithmetic needs.
+  int64_t* queue = queues + warp * 36;
+  int* walk = reinterpret_cast<int*>(queue + 32);
+  const int r0 = find_req(pre, a.reqs, u0);
+  if (lane == 0) walk[0] = (int)u0, walk[1] = -1, walk[2] = r0;
+  __syncwarp();
+  int qn = 0, qi = 0;
   uint32_t badmask = 0;  // stages whose tile has no page
-  auto fetch = [&]() {
-    while (pr.i >= pr.s.k1) {
-      if (pr.next >= u1) {
-        pr.any = false;
-        return;
+  auto refill = [&]() {
+    qn = qi = 0;
+    uint32_t pu = (uint32_t)walk[0];
+    int pk = walk[1], r = walk[2];
+    while (pu < u1) {
+      const Seg s = open_seg(a, RN, pre, lens, starts, r, pu, u1);
+      r = s.r;
+      const int k = pk < 0 ? s.k0 + warp : pk;
+      const int n = k < s.k1 ? min(32, (s.k1 - k + kWarps - 1) / kWarps) : 0;
+      if (lane < n) {
+        const int kk = k + kWarps * lane, tile = kk < s.q.ns ? kk : kk + s.q.off;
+        int64_t at = -1;
+        if (tile < s.q.T) {
+          const int e = (int)(((uint64_t)(uint32_t)tile * a.page_magic) >> 34);
+          const int page = a.table[s.r * a.stride + e];
+          if ((uint64_t)(int64_t)page < (uint64_t)a.n_pages)
+            at = (((int64_t)page * a.heads + s.h) * a.page_tiles + (tile - e * a.page_tiles)) * G::kTile;
+          else if (a.status)
+            atomicOr(a.status, kStatusBadPage);
+        }
+        queue[lane] = at;
       }
-      pr.s = open_seg(a, RN, pre, lens, starts, pr.s.r, pr.next, u1);
-      pr.next += (uint32_t)(pr.s.k1 - pr.s.k0);
-      pr.i = pr.s.k0 + warp;
-      pr.trow = a.table + pr.s.r * a.stride;
-    }
-    pr.tile = pr.i < pr.s.q.ns ? pr.i : pr.i + pr.s.q.off;
-    pr.page = -1;
-    if (pr.tile < pr.s.q.T) {
-      pr.page = pr.trow[((uint64_t)(uint32_t)pr.tile * a.page_magic) >> 34];
-      if ((uint64_t)(int64_t)pr.page >= (uint64_t)a.n_pages) {
-        pr.page = -1;
-        if (lane == 0 && a.status) atomicOr(a.status, kStatusBadPage);
+      pk = k + kWarps * n;
+      if (pk >= s.k1) pu += (uint32_t)(s.k1 - s.k0), pk = -1;
+      if (n) {
+        qn = n;
+        break;
       }
     }
-    pr.i += kWarps;
-    pr.any = true;
+    __syncwarp();
+    if (lane == 0) walk[0] = (int)pu, walk[1] = pk, walk[2] = r;
+    __syncwarp();
   };
   auto issue = [&](int stage) {
-    if (!pr.any) return;
-    const bool ok = pr.page >= 0;
-    badmask = ok ? badmask & ~(1u << stage) : badmask | 1u << stage;
+    if (qi == qn) refill();
+    if (qn == 0) return;
+    const int64_t at = queue[qi++];
+    badmask = at >= 0 ? badmask & ~(1u << stage) : badmask | 1u << stage;
     if (lane == 0) {
-      if (ok) {
-        const uint32_t e = (uint32_t)(((uint64_t)(uint32_t)pr.tile * a.page_magic) >> 34);
-        const int64_t at = ((int64_t)pr.page * a.heads + pr.s.h) * a.page_tiles +
-                           (pr.tile - (int)e * a.page_tiles);
+      if (at >= 0) {
         mbar_expect_tx(bar + stage, G::kTile);
-        bulk_load(wring + stage * G::kTile, a.cache + at * G::kTile, G::kTile, bar + stage);
+        bulk_load(wring + stage * G::kTile, a.cache + at, G::kTile, bar + stage);
       } else {
         mbar_arrive(bar + stage);
       }
     }
-    fetch();
+    __syncwarp();
   };
-  pr.s.r = find_req(pre, a.reqs, u0);
-  pr.s.k1 = 0;
-  pr.i = 0;
-  pr.next = u0;
-  pr.any = false;
-  fetch();
   for (int i = 0; i < G::kStages; ++i) issue(i);
 
   int stage = 0;
@@ -589,13 +618,18 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
   uint32_t qr[G::kQReg ? NB : 1][NT][4];
   float qs[NT][2];
 
-  int r = find_req(pre, a.reqs, u0);
+  int r = r0;
+  int* part = notes;
   for (uint32_t u = u0; u < u1;) {
     const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
-    r = s.r;
     const int row0 = starts[s.r];
     const int nrow = min(RN, s.q.nq * a.G - s.j * RN);  // rows of this item
     const int first = s.j * RN;
+    if (tid == 0) {  // for the end of the part
+      part[0] = row0, part[1] = nrow, part[2] = first, part[3] = s.h;
+      part[4] = s.k0 == 0 ? 1 : 0, part[5] = s.k0 == 0 && s.k1 == s.q.n ? 1 : 0;
+      part[6] = (int)(u + (uint32_t)(s.k1 - s.k0)), part[7] = s.r;
+    }
 
     // ---- the item's queries: f16 times a power of two for each row
 #pragma unroll 1
@@ -626,7 +660,7 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
       ab = __reduce_max_sync(~0u, ab);
       // largest magnitude to [2^14, 2^15); rows with an infinity or a NaN are left as they are
       const int ex = ab >= 0x7F800000u ? 14 : max((int)(ab >> 23), 1) - 127;
-      const int up = 14 - ex, up1 = up / 2;
+      const int up = min(14 - ex, 110), up1 = up / 2;
       const float f1 = mtail::exp2_int(up1), f2 = mtail::exp2_int(up - up1);
       uint8_t* dst = sq + i * G::kQRow + lane * E * 2;
 #pragma unroll
@@ -634,7 +668,7 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
         reinterpret_cast<uint32_t*>(dst)[k] = pack_f16(x[2 * k] * f1 * f2, x[2 * k + 1] * f1 * f2);
       if (lane == 0) {
         rowpos[i] = i < nrow ? s.q.L - s.q.nq + tok : INT32_MIN / 2;
-        sqs[i] = a.scale_log2 * exp2f((float)(ex - 14));
+        sqs[i] = fmaxf(a.scale_log2 * mtail::exp2_int(-up), 1.4e-45f);  // (0 * -inf is a NaN)
       }
     }
     __syncthreads();
@@ -656,7 +690,7 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      st.lo[b] = kUnset;
+      st.lo4[b] = 0;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -664,24 +698,22 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) st.o[b][mt][nt][e] = 0.f;
     }
+    st.placed = false;
     const int pmin = s.q.L - s.q.nq + first / a.G, pmax = s.q.L - s.q.nq + (first + nrow - 1) / a.G;
 
     // ---- this warp's tiles of the part
-    for (int k = s.k0 + warp; k < s.k1; k += kWarps) {
-      if (!dead && !mbar_wait(bar + stage, phase, kBudgetNs)) {
+    const int k1 = s.k1, ns = s.q.ns, off = s.q.off;
+    for (int k = s.k0 + warp; k < k1; k += kWarps) {
+      if (!dead && !__all_sync(~0u, tile_wait(bar + stage, phase))) {
         if (lane == 0 && a.status) atomicOr(a.status, kStatusTimeout);
         dead = true;
       }
-      dead = __any_sync(~0u, dead);
-      const int tile = k < s.q.ns ? k : k + s.q.off, t0 = tile * 16;
+      const int t0 = (k < ns ? k : k + off) * 16;
       if (!dead) {
         const uint8_t* tp = wring + stage * G::kTile;
         if (!(badmask >> stage & 1) && t0 <= pmax) {
           const bool full = t0 + 15 <= pmin && (a.window == 0 || t0 > pmax - a.window || t0 + 15 < a.sinks);
-          if (full)
-            tile_step<D, NT, false>(st, tp, sq, qr, qs, rowpos, t0, pmax, a.window, a.sinks);
-          else
-            tile_step<D, NT, true>(st, tp, sq, qr, qs, rowpos, t0, pmax, a.window, a.sinks);
+          tile_step<D, NT>(st, tp, sq, qr, qs, rowpos, !full, t0, pmax, a.window, a.sinks);
         }
         __syncwarp();
         issue(stage);
@@ -705,7 +737,7 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
       }
     if (lane == 0) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xlo[warp * NB + b] = st.lo[b];
+      for (int b = 0; b < NB; ++b) xlo[warp * NB + b] = st.placed ? (int)(st.lo4[b] & 255) : -1;
     }
     __syncthreads();
     float lsum[NT][2];
@@ -737,7 +769,7 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
       lomax[b] = xlo[b];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) lomax[b] = max(lomax[b], xlo[w * NB + b]);
-      if (st.lo[b] >= 0) scale_block(st, b, exp2f((float)(st.lo[b] - lomax[b])));
+      if (st.placed) scale_block(st, b, exp2f((float)((int)(st.lo4[b] & 255) - lomax[b])));
     }
     float* of = &st.o[0][0][0][0];
     if (warp >= 2) {
@@ -755,8 +787,9 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
     }
     __syncthreads();
     if (warp == 0) {
-      const bool whole = s.k0 == 0 && s.k1 == s.q.n;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (s.k0 == 0 ? 1 : 0);
+      const int row0 = part[0], nrow = part[1], first = part[2], h = part[3];
+      const bool whole = part[5] != 0;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + part[4];
       float* po = a.part + slot * RN * D;
       float* pml = a.part + 2 * (int64_t)a.ctas * RN * D + slot * RN * 2;
 #pragma unroll
@@ -769,7 +802,7 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
           const float inv = lsum[nt][e] == 0.f ? 0.f : 1.f / lsum[nt][e];
           if (i >= nrow) continue;
           const int rho = first + i, tok = rho / a.G;
-          uint16_t* orow = a.out + (row0 + tok) * a.ldo + (int64_t)(s.h * a.G + rho - tok * a.G) * D;
+          uint16_t* orow = a.out + (row0 + tok) * a.ldo + (int64_t)(h * a.G + rho - tok * a.G) * D;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const float f = inv * mtail::exp2_int(max(lomax[b], 0) + 14 - 127);
@@ -786,12 +819,14 @@ k_kv4_attn(const __grid_constant__ AttnArgs a) {
           if (!whole && g == 0) *reinterpret_cast<float2*>(pml + 2 * i) = make_float2(st.m[nt][e], lsum[nt][e]);
         }
     }
-    u += (uint32_t)(s.k1 - s.k0);
+    u = (uint32_t)part[6];
+    r = part[7];
+    part = part == notes ? notes + 8 : notes;  // (a warp may still be reading these)
   }
 
   if (dead) {  // let the copies in flight land before the shared memory goes
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_wait(bar + stage, phase, kBudgetNs);
+      tile_wait(bar + stage, phase);
       if (++stage == G::kStages) stage = 0, phase ^= 1;
     }
   }
