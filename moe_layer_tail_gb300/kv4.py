@@ -39,96 +39,108 @@ def declare(lib):
     lib.moe_kv4_attention_workspace.restype = i64
 
 
-def _lib():
-    from . import load_library
-    return load_library()
-
-
 def _refuse(what, why):
     from . import ERR_INVALID_ARG, MoeTailError
     raise MoeTailError(ERR_INVALID_ARG, "%s: %s" % (what, why))
 
 
-def _done(rc, what):
+def _failed(rc, what):
+    from . import MoeTailError
+    raise MoeTailError(rc, what)
+
+
+# The checks below run on every call of a decode step, so they stay close to the bare attribute
+# reads: a step of small kernels is otherwise bound by its host side.
+
+_torch = None
+_library = None
+
+
+def _begin(what, anchor):
+    """(torch, the library, the CUDA device index of `anchor`)."""
+    global _torch, _library
+    if _library is None:
+        import torch
+        from . import load_library
+        _torch, _library = torch, load_library()
+    dev = anchor.get_device()
+    if dev < 0:
+        _refuse(what, "needs CUDA tensors")
+    return _torch, _library, dev
+
+
+def _wrong(what, name, t, dtype, dev):
+    if not getattr(t, "is_cuda", False) or t.get_device() != dev:
+        _refuse(what, "%s must be a CUDA tensor on cuda:%d" % (name, dev))
+    _refuse(what, "%s must be %s, is %s" % (name, dtype, t.dtype))
+
+
+def _flat(what, name, t, dtype, dev, n, more=False):
+    """The address of a contiguous 1-D tensor of n elements (or more)."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _wrong(what, name, t, dtype, dev)
+    have = t.numel()
+    if t.dim() != 1 or not t.is_contiguous() or (have < n if more else have != n):
+        _refuse(what, "%s must be contiguous with %s%d elements, has shape %s"
+                % (name, "at least " if more else "", n, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _rows(what, name, t, dtype, dev, heads, dim, rows):
+    """The address and row stride of [>= rows, heads, dim] whose rows are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _wrong(what, name, t, dtype, dev)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or shape[0] < rows:
+        _refuse(what, "%s has shape %s, expected [>= %d, %d, %d]"
+                % (name, tuple(shape), rows, heads, dim))
+    ld, sh, sd = t.stride()
+    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
+        _refuse(what, "%s: a row's heads must be contiguous" % name)
+    if shape[0] == 1 and ld < heads * dim:
+        ld = heads * dim  # (one row: its stride says nothing)
+    return t.data_ptr(), ld
+
+
+def _table(what, t, dev, reqs, i32):
+    """The address, width and row stride of a block table [>= reqs, width]."""
+    if t.dtype is not i32 or t.get_device() != dev:
+        _wrong(what, "block_table", t, i32, dev)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < reqs or shape[1] < 1 or (shape[1] > 1 and t.stride(1) != 1):
+        _refuse(what, "block_table must be [>= %d, width] with contiguous rows, has shape %s"
+                % (reqs, tuple(shape)))
+    ld = t.stride(0)
+    if ld < shape[1]:
+        if shape[0] > 1:
+            _refuse(what, "block_table: rows overlap")
+        ld = shape[1]
+    return t.data_ptr(), shape[1], ld
+
+
+def _cache(what, t, dev, u8):
+    """The address, pages, kv heads, page size and head dim of a cache tensor."""
+    if t.dtype is not u8 or t.get_device() != dev:
+        _wrong(what, "cache", t, u8, dev)
+    shape = t.shape
+    if len(shape) != 4 or shape[3] % 17 or 0 in shape or not t.is_contiguous():
+        _refuse(what, "cache must be contiguous uint8 [pages, kv_heads, page_size / 16, "
+                "17 * head_dim], has shape %s" % (tuple(shape),))
+    return t.data_ptr(), shape[0], shape[1], shape[2] * 16, shape[3] // 17
+
+
+def _launch(what, torch, dev, stream, call):
+    """Run call(raw stream) with `dev` current, on its current stream or the given one."""
+    if stream is not None and stream.device.index != dev:
+        _refuse(what, "stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    if torch._C._cuda_getDevice() == dev:
+        rc = call(torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                      else stream.cuda_stream)
     if rc:
-        from . import MoeTailError
-        raise MoeTailError(rc, what)
-
-
-class _Call:
-    """The tensors of one call: each checked for type, shape and device as it is added."""
-
-    def __init__(self, what, anchor):
-        self.what = what
-        if not getattr(anchor, "is_cuda", False):
-            _refuse(what, "needs CUDA tensors")
-        self.device = anchor.device
-
-    def _check(self, name, t, dtype):
-        if not getattr(t, "is_cuda", False) or t.device != self.device:
-            _refuse(self.what, "%s must be a CUDA tensor on %s" % (name, self.device))
-        if t.dtype != dtype:
-            _refuse(self.what, "%s must be %s, is %s" % (name, dtype, t.dtype))
-
-    def flat(self, name, t, dtype, n, at_least=False):
-        """A contiguous 1-D tensor of n elements (or more)."""
-        if t is None:
-            return None
-        self._check(name, t, dtype)
-        if t.dim() != 1 or not t.is_contiguous() or (t.numel() < n if at_least else t.numel() != n):
-            _refuse(self.what, "%s must be contiguous with %s%d elements, has shape %s"
-                    % (name, "at least " if at_least else "", n, tuple(t.shape)))
-        return t.data_ptr()
-
-    def rows(self, name, t, dtype, heads=None, dim=None, rows=None):
-        """[rows, heads, dim] whose rows are contiguous: (pointer, row stride)."""
-        self._check(name, t, dtype)
-        if (t.dim() != 3 or (heads is not None and t.shape[1] != heads)
-                or (dim is not None and t.shape[2] != dim)
-                or (rows is not None and t.shape[0] < rows)):
-            _refuse(self.what, "%s has shape %s, expected [%s, %s, %s]"
-                    % (name, tuple(t.shape), "rows" if rows is None else ">= %d" % rows,
-                       "heads" if heads is None else heads, "head_dim" if dim is None else dim))
-        if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            _refuse(self.what, "%s: a row's heads must be contiguous" % name)
-        ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
-        return t.data_ptr(), ld
-
-    def table(self, name, t, reqs):
-        import torch
-        self._check(name, t, torch.int32)
-        if t.dim() != 2 or t.shape[0] < reqs or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
-            _refuse(self.what, "%s must be [>= %d, width] with contiguous rows, has shape %s"
-                    % (name, reqs, tuple(t.shape)))
-        ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-        if ld < t.shape[1]:
-            _refuse(self.what, "%s: rows overlap" % name)
-        return t.data_ptr(), t.shape[1], ld
-
-    def cache(self, t):
-        """(pointer, pages, kv heads, page size, head dim) of a cache tensor."""
-        import torch
-        self._check("cache", t, torch.uint8)
-        if t.dim() != 4 or not t.is_contiguous() or t.shape[3] % 17 or 0 in t.shape:
-            _refuse(self.what, "cache must be contiguous uint8 [pages, kv_heads, page_size / 16, "
-                    "17 * head_dim], has shape %s" % (tuple(t.shape),))
-        return t.data_ptr(), t.shape[0], t.shape[1], t.shape[2] * 16, t.shape[3] // 17
-
-    def status(self, t):
-        import torch
-        return None if t is None else self.flat("status", t, torch.int32, 1)
-
-    def stream(self, stream):
-        import torch
-        if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        if stream.device != self.device:
-            _refuse(self.what, "stream is on %s, the tensors on %s" % (stream.device, self.device))
-        return stream.cuda_stream
-
-    def guard(self):
-        import torch
-        return torch.cuda.device(self.device)
+        _failed(rc, "moe_" + what)
 
 
 def kv4_cache(n_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -145,23 +157,26 @@ def kv4_cache(n_pages: int, page_size: int, kv_heads: int, head_dim: int, device
 def step_tables(cached_lens, new_lens, free_pages, block_table, page_size: int, row_starts,
                 kv_lens, positions, slots, pages_used, status=None, stream=None) -> None:
     """Block tables, row starts, positions and slots of one step from the requests' lengths
-    (moe_step_tables).  cached_lens, new_lens int32 [reqs]; free_pages int32 [n]; block_table
-    int32 [reqs, width], filled in place; row_starts int32 [reqs + 1], kv_lens int32 [reqs],
-    positions int32 and slots int64 [max_rows], pages_used int32 [1]: written."""
-    import torch
-    c = _Call("step_tables", cached_lens)
+    (moe_step_tables).  cached_lens, new_lens int32 [reqs]; free_pages int32 [n] or None;
+    block_table int32 [reqs, width], filled in place; row_starts int32 [reqs + 1], kv_lens int32
+    [reqs], positions int32 and slots int64 [max_rows], pages_used int32 [1]: written."""
+    w = "step_tables"
+    torch, lib, dev = _begin(w, cached_lens)
     i32 = torch.int32
     reqs, n = cached_lens.numel(), positions.numel()
-    pt, width, ld = c.table("block_table", block_table, reqs)
-    args = [c.flat("cached_lens", cached_lens, i32, reqs), c.flat("new_lens", new_lens, i32, reqs),
-            c.flat("free_pages", free_pages, i32, 0, True), pt,
-            c.flat("row_starts", row_starts, i32, reqs + 1), c.flat("kv_lens", kv_lens, i32, reqs),
-            c.flat("positions", positions, i32, n), c.flat("slots", slots, torch.int64, n),
-            c.flat("pages_used", pages_used, i32, 1), c.status(status)]
     n_free = 0 if free_pages is None else free_pages.numel()
-    with c.guard():
-        _done(_lib().moe_step_tables(reqs, n, int(page_size), n_free, width, ld, *args,
-                                     c.stream(stream)), "moe_step_tables")
+    pt, width, ld = _table(w, block_table, dev, reqs, i32)
+    args = (reqs, n, page_size, n_free, width, ld,
+            _flat(w, "cached_lens", cached_lens, i32, dev, reqs),
+            _flat(w, "new_lens", new_lens, i32, dev, reqs),
+            _flat(w, "free_pages", free_pages, i32, dev, n_free) if n_free else None, pt,
+            _flat(w, "row_starts", row_starts, i32, dev, reqs + 1),
+            _flat(w, "kv_lens", kv_lens, i32, dev, reqs),
+            _flat(w, "positions", positions, i32, dev, n),
+            _flat(w, "slots", slots, torch.int64, dev, n),
+            _flat(w, "pages_used", pages_used, i32, dev, 1),
+            None if status is None else _flat(w, "status", status, i32, dev, 1))
+    _launch(w, torch, dev, stream, lambda st: lib.moe_step_tables(*args, st))
 
 
 def qk_norm_rope(q, k, q_gamma, k_gamma, positions, inv_freq, q_out, k_out, eps: float = 1e-6,
@@ -169,64 +184,70 @@ def qk_norm_rope(q, k, q_gamma, k_gamma, positions, inv_freq, q_out, k_out, eps:
     """RMSNorm of every query and key head and the position rotation (moe_qk_norm_rope): q
     [rows, q_heads, D] and k [rows, k_heads, D] bf16 (or k, k_out None) with any row stride,
     gammas bf16 [D] or None (no norm on that side), positions int32 [rows], inv_freq float32
-    [rot_dim / 2]; q_out may be q and k_out k."""
-    import torch
-    c = _Call("qk_norm_rope", q)
+    [rot_dim / 2] (None: no rotation); q_out may be q and k_out k."""
+    w = "qk_norm_rope"
+    torch, lib, dev = _begin(w, q)
     bf = torch.bfloat16
-    pq, ldq = c.rows("q", q, bf)
+    if q.dim() != 3:
+        _refuse(w, "q must be [rows, heads, head_dim], has shape %s" % (tuple(q.shape),))
     T, hq, D = q.shape
-    pqo, ldqo = c.rows("q_out", q_out, bf, hq, D, T)
+    pq, ldq = _rows(w, "q", q, bf, dev, hq, D, T)
+    pqo, ldqo = _rows(w, "q_out", q_out, bf, dev, hq, D, T)
     hk, pk, ldk, pko, ldko = 0, None, 0, None, 0
     if k is not None:
-        pk, ldk = c.rows("k", k, bf, None, D, T)
-        hk = k.shape[1]
-        if k_out is None:
-            _refuse("qk_norm_rope", "k without k_out")
-        pko, ldko = c.rows("k_out", k_out, bf, hk, D, T)
-    gq = c.flat("q_gamma", q_gamma, bf, D)
-    gk = c.flat("k_gamma", k_gamma, bf, D)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    pos = c.flat("positions", positions, torch.int32, T, True)
-    fr = c.flat("inv_freq", inv_freq, torch.float32, rot // 2)
-    with c.guard():
-        _done(_lib().moe_qk_norm_rope(T, hq, hk, D, rot, int(bool(interleaved)), float(eps), pq, ldq,
-                                      pk, ldk, gq, gk, pos, fr, pqo, ldqo, pko, ldko,
-                                      c.stream(stream)), "moe_qk_norm_rope")
+        if k_out is None or k.dim() != 3:
+            _refuse(w, "k must be [rows, heads, head_dim] and come with k_out")
+        hk = k.size(1)
+        pk, ldk = _rows(w, "k", k, bf, dev, hk, D, T)
+        pko, ldko = _rows(w, "k_out", k_out, bf, dev, hk, D, T)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    args = (T, hq, hk, D, 2 * half, 1 if interleaved else 0, eps, pq, ldq, pk, ldk,
+            None if q_gamma is None else _flat(w, "q_gamma", q_gamma, bf, dev, D),
+            None if k_gamma is None else _flat(w, "k_gamma", k_gamma, bf, dev, D),
+            None if positions is None else _flat(w, "positions", positions, torch.int32, dev, T, True),
+            None if not half else _flat(w, "inv_freq", inv_freq, torch.float32, dev, half),
+            pqo, ldqo, pko, ldko)
+    _launch(w, torch, dev, stream, lambda st: lib.moe_qk_norm_rope(*args, st))
 
 
-def _cache_rows(what, fn, cache, k, v, slots, status, stream):
-    import torch
-    c = _Call(what, cache)
-    pc, n_pages, heads, page, D = c.cache(cache)
+def _cache_rows(w, torch, lib, dev, fn, cache, k, v, slots, status, stream):
+    bf = torch.bfloat16
+    pc, n_pages, heads, page, D = _cache(w, cache, dev, torch.uint8)
     T = slots.numel()
-    ps = c.flat("slots", slots, torch.int64, T)
-    pk, ldk = c.rows("k", k, torch.bfloat16, heads, D, T)
-    pv, ldv = c.rows("v", v, torch.bfloat16, heads, D, T)
-    with c.guard():
-        _done(fn(T, heads, D, page, n_pages, pc, pk, ldk, pv, ldv, ps, c.status(status),
-                 c.stream(stream)), "moe_" + what)
+    ps = _flat(w, "slots", slots, torch.int64, dev, T)
+    pk, ldk = _rows(w, "k", k, bf, dev, heads, D, T)
+    pv, ldv = _rows(w, "v", v, bf, dev, heads, D, T)
+    st = None if status is None else _flat(w, "status", status, torch.int32, dev, 1)
+    _launch(w, torch, dev, stream,
+            lambda s: fn(T, heads, D, page, n_pages, pc, pk, ldk, pv, ldv, ps, st, s))
 
 
 def kv4_append(cache, k, v, slots, status=None, stream=None) -> None:
     """Quantise k, v bf16 [rows, kv_heads, D] (any row stride) into slots int64 [rows] of the
     cache (moe_kv4_append); negative slots are skipped."""
-    _cache_rows("kv4_append", _lib().moe_kv4_append, cache, k, v, slots, status, stream)
+    torch, lib, dev = _begin("kv4_append", cache)
+    _cache_rows("kv4_append", torch, lib, dev, lib.moe_kv4_append, cache, k, v, slots, status, stream)
 
 
 def kv4_read(cache, slots, k, v, status=None, stream=None) -> None:
     """The cache's values in slots int64 [rows] into k, v bf16 [rows, kv_heads, D] (exact)."""
-    _cache_rows("kv4_read", _lib().moe_kv4_read, cache, k, v, slots, status, stream)
+    torch, lib, dev = _begin("kv4_read", cache)
+    _cache_rows("kv4_read", torch, lib, dev, lib.moe_kv4_read, cache, k, v, slots, status, stream)
+
+
+_workspace_bytes = {}  # (device, q heads, kv heads, head dim, max_new) -> bytes
 
 
 def kv4_attention_workspace(q_heads: int, kv_heads: int, head_dim: int, max_new: int = 1,
                             device=None) -> int:
     """Bytes of workspace that kv4_attention needs on `device` (default: the current one)."""
     import torch
+    from . import load_library
     with torch.cuda.device(device):
-        n = _lib().moe_kv4_attention_workspace(int(q_heads), int(kv_heads), int(head_dim),
-                                               int(max_new))
+        n = load_library().moe_kv4_attention_workspace(int(q_heads), int(kv_heads), int(head_dim),
+                                                       int(max_new))
     if n < 0:
-        _done(int(n), "moe_kv4_attention_workspace")
+        _failed(int(n), "moe_kv4_attention_workspace")
     return int(n)
 
 
@@ -240,26 +261,33 @@ def kv4_attention(q, cache, block_table, row_starts, kv_lens, out, scale: float 
     kv4_attention_workspace bytes, not shared with a call that may run at the same time (two
     captured graphs replayed in different streams need two); None takes one from PyTorch's
     allocator for this call."""
-    import torch
-    c = _Call("kv4_attention", q)
-    pc, n_pages, heads, page, D = c.cache(cache)
-    pq, ldq = c.rows("q", q, torch.bfloat16, None, D)
-    T, hq = q.shape[0], q.shape[1]
-    po, ldo = c.rows("out", out, torch.bfloat16, hq, D, T)
+    w = "kv4_attention"
+    torch, lib, dev = _begin(w, q)
+    i32, bf = torch.int32, torch.bfloat16
+    pc, n_pages, heads, page, D = _cache(w, cache, dev, torch.uint8)
+    if q.dim() != 3:
+        _refuse(w, "q must be [rows, heads, head_dim], has shape %s" % (tuple(q.shape),))
+    T, hq, _ = q.shape
+    pq, ldq = _rows(w, "q", q, bf, dev, hq, D, T)
+    po, ldo = _rows(w, "out", out, bf, dev, hq, D, T)
     reqs = kv_lens.numel()
-    pt, width, ld = c.table("block_table", block_table, reqs)
-    prs = c.flat("row_starts", row_starts, torch.int32, reqs + 1)
-    pkl = c.flat("kv_lens", kv_lens, torch.int32, reqs)
-    with c.guard():
-        lib = _lib()
-        if workspace is None:
-            n = kv4_attention_workspace(hq, heads, D, max_new, c.device)
-            # memory of the launching stream: the allocator reuses it only behind this call
+    pt, width, ld = _table(w, block_table, dev, reqs, i32)
+    prs = _flat(w, "row_starts", row_starts, i32, dev, reqs + 1)
+    pkl = _flat(w, "kv_lens", kv_lens, i32, dev, reqs)
+    st = None if status is None else _flat(w, "status", status, i32, dev, 1)
+    if workspace is None:
+        key = (dev, hq, heads, D, max_new)
+        n = _workspace_bytes.get(key)
+        if n is None:
+            n = _workspace_bytes[key] = kv4_attention_workspace(hq, heads, D, max_new, dev)
+        if stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        else:  # memory of the launching stream: the allocator reuses it only behind this call
             with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=torch.uint8, device=c.device)
-        pw = c.flat("workspace", workspace, torch.uint8, 0, True)
-        _done(lib.moe_kv4_attention(T, reqs, hq, heads, D, page, n_pages, pq, ldq, pc, pt, width, ld,
-                                    prs, pkl, float(D ** -0.5 if scale is None else scale),
-                                    int(window), int(sinks), int(max_new), po, ldo, pw,
-                                    workspace.numel(), c.status(status), c.stream(stream)),
-              "moe_kv4_attention")
+                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    n = workspace.numel()
+    pw = _flat(w, "workspace", workspace, torch.uint8, dev, n)
+    sc = D ** -0.5 if scale is None else scale
+    _launch(w, torch, dev, stream, lambda s: lib.moe_kv4_attention(
+        T, reqs, hq, heads, D, page, n_pages, pq, ldq, pc, pt, width, ld, prs, pkl, sc, window, sinks,
+        max_new, po, ldo, pw, n, st, s))
