@@ -1,0 +1,118 @@
+// k_kv4_plan.cuh -- how the attention over the MXFP4 cache cuts its work: items, ranges, parts.
+// Internal to libmoe_tail.so.
+//
+// A work item is one request's query rows of one kv head, RN rows at a time; its tiles of 16
+// tokens, laid end to end over all items, are cut into equal ranges, one per CTA.  A part is what
+// an item and a range have in common.
+#pragma once
+
+#include "k_kv4.cuh"
+
+namespace kv4 {
+
+constexpr int kMinTiles = 8;  // of a range
+
+struct Req {
+  int L, nq, rt;   // cache length, query rows, items per kv head
+  int ns, off, T;  // tiles of first tokens, then off further; tiles of the whole length
+  int n;           // tiles of an item
+};
+
+// A request's work; nq = 0 (and *bits) when its row starts are not usable.
+__device__ __forceinline__ Req req_of(const AttnArgs& a, int rn, int L, int rs, int re, int* bits) {
+  Req q;
+  if (L < 0 || L > a.max_len) *bits |= kStatusBadLength;
+  q.L = max(0, min(L, a.max_len));
+  if (rs < 0 || re < rs || re > a.rows) *bits |= kStatusBadLength, re = rs;
+  q.nq = re - rs;
+  q.rt = (int)(((int64_t)q.nq * a.G + rn - 1) / rn);
+  q.T = (int)(((uint32_t)q.L + 15u) >> 4);
+  q.ns = q.off = 0;
+  int fw = 0;
+  if (a.window > 0) {
+    const int64_t f = (int64_t)q.L - q.nq - a.window + 1;  // first token of the first row's window
+    fw = f > 0 ? (int)(f >> 4) : 0;
+    q.ns = (int)min((int64_t)fw, ((int64_t)a.sinks + 15) >> 4);
+    q.off = fw - q.ns;
+  }
+  q.n = max(1, q.ns + q.T - fw);
+  return q;
+}
+
+// Sums the work of all requests: pre[r] = tiles before request r (shared), the lengths and row
+// starts beside it.  Returns all tiles (the same in every one of the CTA's 32 W threads).
+template <int W>
+__device__ __forceinline__ uint64_t plan(const AttnArgs& a, int rn, uint32_t* pre, int* lens,
+                                         int* starts, uint64_t* wsum, int* bits) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t base = 0;
+  for (int r0 = 0; r0 < a.reqs; r0 += 32 * W) {
+    const int r = r0 + tid;
+    uint64_t v = 0;
+    if (r < a.reqs) {
+      const int L = a.kv_lens[r], rs = a.row_starts[r], re = a.row_starts[r + 1];
+      const Req q = req_of(a, rn, L, rs, re, bits);
+      v = (uint64_t)q.rt * (uint32_t)a.heads * (uint32_t)q.n;
+      lens[r] = L;
+      starts[r] = rs;
+      if (r == a.reqs - 1) starts[a.reqs] = re;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t w = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += w;
+    }
+    if (lane == 31) wsum[warp] = v;
+    __syncthreads();
+    uint64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) v += wsum[w];
+      all += wsum[w];
+    }
+    if (r < a.reqs) pre[r + 1] = (uint32_t)(base + v);
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[0] = 0;
+  __syncthreads();
+  return base;
+}
+__device__ __forceinline__ uint32_t range_tiles(uint64_t total, int ctas) {
+  return max((uint32_t)((total + ctas - 1) / ctas), (uint32_t)kMinTiles);
+}
+__device__ __forceinline__ int find_req(const uint32_t* pre, int reqs, uint32_t u) {
+  int lo = 0, hi = reqs - 1;
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (pre[m] <= u) lo = m; else hi = m - 1;
+  }
+  while (lo < reqs - 1 && pre[lo + 1] <= u) ++lo;  // (requests without work)
+  return lo;
+}
+
+// One item's part of a CTA's range.
+struct Seg {
+  int r, h, j;      // request, kv head, block of RN rows
+  int k0, k1;       // its tiles of the item's q.n
+  uint32_t item;    // the range-wide number of the item's first tile
+  Req q;
+};
+__device__ __forceinline__ Seg open_seg(const AttnArgs& a, int rn, const uint32_t* pre,
+                                        const int* lens, const int* starts, int r, uint32_t u,
+                                        uint32_t u1) {
+  Seg s;
+  while (r < a.reqs - 1 && pre[r + 1] <= u) ++r;
+  int bits = 0;
+  s.r = r;
+  s.q = req_of(a, rn, lens[r], starts[r], starts[r + 1], &bits);
+  const uint32_t local = u - pre[r], item = local / (uint32_t)s.q.n;
+  s.k0 = (int)(local - item * (uint32_t)s.q.n);
+  s.item = u - (uint32_t)s.k0;
+  s.h = (int)(item / (uint32_t)s.q.rt);
+  s.j = (int)(item - (uint32_t)s.h * (uint32_t)s.q.rt);
+  s.k1 = (int)min((uint32_t)s.q.n, (uint32_t)s.k0 + (u1 - u));
+  return s;
+}
+
+}  // namespace kv4

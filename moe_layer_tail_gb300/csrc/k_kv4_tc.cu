@@ -1,0 +1,928 @@
+// k_kv4_tc.cu -- attention of a step's query rows over the paged MXFP4 cache (kv4_attn.h) on the
+// tcgen05 tensor cores.
+//
+//   out[i] = sum_j p_j V_j / sum_j p_j,  p_j = 2^(scale log2(e) q_i . K_j - m_i)
+//
+// in one pass over the cache.  The query heads that share a kv head, and the rows of a request,
+// are rows of one work item (RN at a time), so the cache is read once for all of them; the items'
+// tiles of 16 tokens, laid end to end, are cut into equal ranges, one per SM (k_kv4_plan.cuh), so
+// that ragged lengths, one long request and many short ones all load every SM the same.  An item
+// that lies in one range is written by its CTA; the others leave an average and (max, sum) per row
+// and part in the workspace, which a second launch joins (programmatic dependent launch).
+//
+// The CUDA cores never see a key or a value.  A step is 8 tiles (128 tokens) of one kv head:
+//   K' [128 tokens x D] = K I      tcgen05 kind::mxf4 block-scaled, the codes and scales as they
+//                                  are cached times an E2M1 identity: the dequantised keys, exact
+//                                  fp32, in tensor memory;
+//   S^T [128 x RN] = K' Q^T        kind::tf32, K' read from tensor memory as operand A, the bf16
+//                                  queries exact as tf32 in shared memory;
+//   P^T = 2^(S - m)                fp32 on the CUDA cores, a token per thread, rounded to tf32 (the
+//                                  row's sum adds the rounded numerators, so the rounding has no
+//                                  bias); m is the maximum over the item's first step and moves
+//                                  again only when a score passes it by 40 octaves;
+//   V' [D x 128 tokens] = I V^T    the dequantised values, transposed by the product itself;
+//   O^T [D x RN] += V' P^T         kind::tf32, V' from tensor memory, accumulating there.
+// On a GB300 the products of one step (D 128, RN 16) take 2 x 126 + 2 x 150 of the 740 cycles in
+// which its 17 KB arrive at the measured copy rate; conversions on the CUDA cores into mma.sync
+// had taken 490 warp instructions per tile and stayed at 2.5 TB/s.
+//
+// Warps: 0 looks up pages and copies tiles (bulk copies into a ring, 32 look-ups at a time);
+// 6..13 (one per tile of a step) bring a tile's bytes, which the cache holds in the order of
+// register fragments, into the swizzled rows and scale-factor atoms of the tensor cores' operands;
+// 1 issues the products (one elected thread: a divergent issuer costs 45 cycles an instruction, an
+// elected one 9 at these sizes); 2..5 are the softmax and the output.  They hand over through
+// mbarriers; every wait is bounded and reports MOE_TAIL_STATUS_TIMEOUT.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "k_kv4_plan.cuh"
+#include "k_stream_common.cuh"
+
+namespace kv4 {
+
+using mtail::bulk_load;
+using mtail::mbar_arrive;
+using mtail::mbar_expect_tx;
+using mtail::mbar_init;
+using mtail::mbar_try_wait;
+using mtail::smem_u32;
+
+namespace {
+
+constexpr int kWarps = 14, kThreads = 32 * kWarps;
+constexpr int kLayWarp = 6;  // (0 copies, 1 products, 2..5 softmax)
+constexpr int kStepTiles = 8;
+constexpr int kInfos = 8;                     // steps whose notes are kept
+constexpr int64_t kBudgetClocks = 200000000;  // of a wait, about 0.1 s
+constexpr float kLow = -3.0e38f;              // a row's reference before its first score
+constexpr float kOver = 40.f;                 // octaves above the reference that move it
+constexpr uint32_t kBarSoft = 1;              // named barrier of the softmax warps
+
+// What the softmax needs to know of a step's tokens.
+struct Info {
+  int t0[kStepTiles];     // first token of each tile, negative: the tile has no page
+  uint16_t flags[128];    // of a token: bit 15 a NaN among its key scales, bit b one at value block b
+  int full;               // every row sees every token
+  int pad[3];
+};
+
+template <int D, int RN>
+struct Geo {
+  static constexpr int NM = RN < 16 ? 16 : RN;  // columns of the products
+  static constexpr int NB = D / 32;
+  static constexpr int CH = D < 128 ? D : 128;  // channels of one half
+  static constexpr int kHalves = D / CH;
+  static constexpr int kTile = 17 * D;
+  static constexpr int kStep = kStepTiles * kTile;
+  static constexpr int kRaw = D == 256 ? 2 : D == 128 ? 4 : 6;
+  static constexpr int kOps = D == 256 ? 2 : 3;
+  static constexpr int kQs = D == 256 ? 1 : 2;
+  static constexpr int kOp = D == 256 ? 32768 : 16384;  // codes of a step: rows of 128 bytes
+  static constexpr int kAtoms = D == 256 ? 2 : 1;
+  static constexpr int kSf = 2 * kAtoms * 512;           // key atoms, then value atoms
+  static constexpr int kP = NM * 512, kQ = NM * D * 4;
+  // tensor-memory columns
+  static constexpr int cK = 0, cV = 128, cS = 384, cO = cS + 2 * NM;
+  static constexpr int cSfK = cO + kHalves * NM, cSfV = cSfK + 8 * kAtoms, cSfI = cSfV + 8 * kAtoms;
+  static_assert(cSfI + 4 <= 512, "tensor memory");
+  // shared memory (from a 1024-byte boundary)
+  static constexpr int oOp = 0, oI = oOp + kOps * kOp, oQ = oI + 16384, oP = oQ + kQs * kQ;
+  static constexpr int oRaw = oP + 2 * kP, oSf = (oRaw + kRaw * kStep + 127) / 128 * 128;
+  static constexpr int oSfI = oSf + kOps * kSf, oInfo = oSfI + 512;
+  static constexpr int oSmall = oInfo + kInfos * (int)sizeof(Info);
+  // raw and operand rings, info ring, q, and the single ones
+  static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 10;
+  static constexpr int kSmall = kBars * 8 + kRaw * 12 * 4 /* t0, full */ + 4 * RN * 8 /* red, l */ +
+                                RN * 12 /* references, rowpos, nan */ + 64;
+  static constexpr size_t smem(int reqs) {
+    return 1024 + (size_t)oSmall + kSmall + (size_t)(3 * reqs + 2) * 4;
+  }
+};
+
+// ------------------------------------------------------------------ PTX wrappers ----
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+// shared-memory matrix descriptors: K-major rows of 128 bytes under the 128-byte swizzle (8-row
+// groups 1024 bytes apart), and scale-factor atoms (no swizzle)
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t sf_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (8ull << 16) | (8ull << 32) | (1ull << 46);
+}
+// instruction descriptors: E2M1 x E2M1 with UE8M0 scales (the scale bytes of the K step's two
+// blocks from sf_id on), and tf32 x tf32; M 128, N columns, fp32 accumulators
+__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf_id) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (8u << 24) | (sf_id << 29) |
+         (sf_id << 4);
+}
+__device__ __forceinline__ uint32_t idesc_tf32(int N) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void cp_sf(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc));
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
+}
+// A in tensor memory, B in shared memory
+__device__ __forceinline__ void mma_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+#define KV4_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define KV4_W8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// this warp's 32 lanes x 8 consecutive columns (lane = tensor-memory lane)
+__device__ __forceinline__ void ld8(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : KV4_R8(0) : "r"(t));
+}
+__device__ __forceinline__ void st8(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), KV4_W8(0));
+}
+#undef KV4_R8
+#undef KV4_W8
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[N]) {
+  uint32_t r[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 8) ld8(t + i, r + i);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[N]) {
+  uint32_t r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; i += 8) st8(t + i, r + i);
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float to_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kBarSoft) : "memory"); }
+__device__ __forceinline__ bool soft_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(kBarSoft)
+      : "memory");
+  return r != 0;
+}
+// bytes of w that are 255, one bit each
+__device__ __forceinline__ uint32_t ff_bytes(uint32_t w) {
+  const uint32_t f = ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
+  return (f >> 7 & 1) | (f >> 14 & 2) | (f >> 21 & 4) | (f >> 28 & 8);
+}
+
+// The largest of each of N values over the warp: lane l returns that of value l mod N.
+template <int N>
+__device__ __forceinline__ float warp_max_of(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = N / 2; h >= 1; h >>= 1) {
+    const bool up = (lane & h) != 0;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = fmaxf(keep, __shfl_xor_sync(~0u, send, h));
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] = fmaxf(v[0], __shfl_xor_sync(~0u, v[0], o));
+  return v[0];
+}
+template <int N>
+__device__ __forceinline__ float warp_sum_of(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = N / 2; h >= 1; h >>= 1) {
+    const bool up = (lane & h) != 0;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = keep + __shfl_xor_sync(~0u, send, h);
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(~0u, v[0], o);
+  return v[0];
+}
+
+struct Bars {
+  uint64_t *raw_full, *raw_empty, *op_full, *op_empty, *info, *q_full, *q_empty;
+  uint64_t *k_full, *half, *s_full, *p_full, *v_full, *pv;  // half: QK of the first half done
+};
+
+// The record that tells the joining launch which item crosses the end of a range.
+struct JoinRec {
+  int last;   // the last range of the item, negative: none crosses
+  int row0;   // first query row of its request
+  int first;  // the item's first row among the request's (row, head) pairs
+  int head;   // kv head
+  int rows;   // rows of the item
+  int pad[3];
+};
+
+template <int D, int RN>
+__global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant__ AttnArgs a) {
+  using G = Geo<D, RN>;
+  constexpr int NM = G::NM, NB = G::NB;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ uint64_t wsum[kWarps];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead;
+  uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+  Info* infos = reinterpret_cast<Info*>(sm + G::oInfo);
+  uint64_t* bp = reinterpret_cast<uint64_t*>(sm + G::oSmall);
+  Bars B;
+  B.raw_full = bp;
+  B.raw_empty = B.raw_full + G::kRaw;
+  B.op_full = B.raw_empty + G::kRaw;
+  B.op_empty = B.op_full + G::kOps;
+  B.info = B.op_empty + G::kOps;
+  B.q_full = B.info + kInfos;
+  B.q_empty = B.q_full + 2;
+  B.k_full = B.q_empty + 2;
+  B.half = B.k_full + 1;
+  B.s_full = B.half + 1;
+  B.p_full = B.s_full + 2;
+  B.v_full = B.p_full + 2;
+  B.pv = B.v_full + 2;
+  int* raw_info = reinterpret_cast<int*>(bp + G::kBars);  // [kRaw][12]: t0 of the tiles, full
+  float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 12);  // [4][RN]
+  float* lsum = red + 4 * RN;                                       // [4][RN]
+  float* mref = lsum + 4 * RN;                                      // [RN]
+  int* rowpos = reinterpret_cast<int*>(mref + RN);
+  uint32_t* nanrow = reinterpret_cast<uint32_t*>(rowpos + RN);
+  uint32_t* pre = nanrow + RN + 16;
+  int* lens = reinterpret_cast<int*>(pre + a.reqs + 1);
+  int* starts = lens + a.reqs;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
+  JoinRec* recs = reinterpret_cast<JoinRec*>(a.part + 2 * (int64_t)a.ctas * RN * (D + 2));
+
+  // ---- set-up that depends on nothing, then the plan
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    s_dead = 0;
+    for (int i = 0; i < G::kBars; ++i) {
+      uint64_t* b = bp + i;
+      const bool lay = (b >= B.raw_empty && b < B.op_empty) || (b >= B.info && b < B.q_empty);
+      mbar_init(b, lay ? 8u : b >= B.p_full && b < B.v_full ? 4u : 1u);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // the identity (E2M1 code 2 is 1.0) in rows of 128 bytes, and its scales
+  for (int i = tid; i < 128 * 8; i += kThreads) {
+    const int r = i >> 3, ch = i & 7;
+    const uint32_t one = ch == r >> 5 ? 2u << (4 * (r & 7)) : 0u;
+    const int w = (r >> 3) & 3;
+    *reinterpret_cast<uint4*>(sm + G::oI + r * 128 + ((ch ^ (r & 7)) << 4)) =
+        make_uint4(w == 0 ? one : 0u, w == 1 ? one : 0u, w == 2 ? one : 0u, w == 3 ? one : 0u);
+  }
+  if (tid < 32) *reinterpret_cast<uint4*>(sm + G::oSfI + tid * 16) = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  fence_proxy();
+
+  int bits = 0;
+  const uint64_t total64 = plan<kWarps>(a, RN, pre, lens, starts, wsum, &bits);
+  if (total64 > 0x7FFFFFFFull) bits |= kStatusBadLength;
+  if (blockIdx.x == 0 && bits && a.status) atomicOr(a.status, bits);
+  const uint32_t total = total64 > 0x7FFFFFFFull ? 0u : (uint32_t)total64, per = range_tiles(total, a.ctas);
+  const uint64_t u0w = (uint64_t)blockIdx.x * per;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = s_tmem;
+  const uint32_t u0 = (uint32_t)min(u0w, (uint64_t)total), u1 = min(total, u0 + per);
+  if (u0 == u1 && tid == 0) recs[blockIdx.x].last = -1;
+
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    if (mbar_try_wait(b, parity & 1)) return;
+    const int64_t t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(b, parity & 1)) return;
+      if (*reinterpret_cast<volatile int*>(&s_dead)) return;
+      if (clock64() - t0 > kBudgetClocks) {
+        *reinterpret_cast<volatile int*>(&s_dead) = 1;
+        if (a.status) atomicOr(a.status, kStatusTimeout);
+        return;
+      }
+    }
+  };
+  auto dead = [&]() { return *reinterpret_cast<volatile int*>(&s_dead) != 0; };
+  const int r0 = u0 < u1 ? find_req(pre, a.reqs, u0) : 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ the tiles' copies ----
+    uint32_t i = 0;
+    int r = r0;
+    for (uint32_t u = u0; u < u1;) {
+      const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+      r = s.r;
+      const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first);
+      const int pmin = s.q.L - s.q.nq + first / a.G, pmax = s.q.L - s.q.nq + (first + nrow - 1) / a.G;
+      for (int k = s.k0; k < s.k1; k += 32) {
+        // a lane looks up one of 32 tiles, the copies of four steps
+        const int kk = k + lane, tile = kk < s.q.ns ? kk : kk + s.q.off;
+        int64_t at = -1;
+        if (kk < s.k1 && tile < s.q.T) {
+          const int e = (int)(((uint64_t)(uint32_t)tile * a.page_magic) >> 34);
+          const int page = a.table[s.r * a.stride + e];
+          if ((uint64_t)(int64_t)page < (uint64_t)a.n_pages)
+            at = (((int64_t)page * a.heads + s.h) * a.page_tiles + (tile - e * a.page_tiles)) * G::kTile;
+          else if (a.status)
+            atomicOr(a.status, kStatusBadPage);
+        }
+        const int t0 = tile * 16;
+        const bool full = at >= 0 && t0 + 15 <= pmin && (a.window == 0 || t0 > pmax - a.window || t0 + 15 < a.sinks);
+        const uint32_t have = __ballot_sync(~0u, at >= 0), fulls = __ballot_sync(~0u, full);
+        const int steps = (min(32, s.k1 - k) + kStepTiles - 1) / kStepTiles;
+        for (int q = 0; q < steps; ++q, ++i) {
+          const int st = (int)(i % G::kRaw);
+          const uint32_t n = i / G::kRaw;
+          if (n > 0) wait(B.raw_empty + st, n - 1);
+          uint8_t* dst = sm + G::oRaw + st * G::kStep;
+          const uint32_t mine = have >> (8 * q) & 255;
+          if (lane >> 3 == q) raw_info[st * 12 + (lane & 7)] = at >= 0 ? t0 : -1;
+          if (lane == 0) raw_info[st * 12 + 8] = (fulls >> (8 * q) & 255) == 255;
+          __syncwarp();
+          const bool go = !dead();
+          if (lane == 0) {
+            if (mine && go) mbar_expect_tx(B.raw_full + st, __popc(mine) * G::kTile);
+            else mbar_arrive(B.raw_full + st);
+          }
+          __syncwarp();
+          if (lane >> 3 == q && at >= 0 && go)
+            bulk_load(dst + (lane & 7) * G::kTile, a.cache + at, G::kTile, B.raw_full + st);
+        }
+      }
+      u += (uint32_t)(s.k1 - s.k0);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------- the tensor cores ----
+    if (elect_one()) {
+      const uint32_t base = smem_u32(sm);
+      const uint64_t dI = sw128_desc(base + G::oI);
+      cp_sf(tm + G::cSfI, sf_desc(base + G::oSfI));
+      uint32_t i = 0, seg = 0, kc = 0;
+      uint32_t firsts = 0;  // bit n & 1: step n began an item's part
+      // dequantised keys of step n, half h (its operands waited for with the first half)
+      auto k_ident = [&](uint32_t n, int h) {
+        const uint32_t op = n % G::kOps;
+        const uint32_t ob = base + G::oOp + op * G::kOp, sb = base + G::oSf + op * G::kSf;
+        if (h == 0) {
+          wait(B.op_full + op, n / G::kOps);
+          fence_after();
+          for (int at = 0; at < G::kAtoms; ++at)
+            cp_sf(tm + G::cSfK + (n & 1) * 4 * G::kAtoms + 4 * at, sf_desc(sb + 512 * at));
+        }
+        const uint64_t dK = sw128_desc(ob);
+#pragma unroll
+        for (int k = 0; k < G::CH / 64; ++k)
+          mma_mxf4(tm + G::cK, dK + (uint64_t)((64 * h + 32 * k) >> 4), dI + (uint64_t)(2 * k),
+                   idesc_mxf4(G::CH, 2 * k), tm + G::cSfK + (n & 1) * 4 * G::kAtoms + 4 * h, tm + G::cSfI, k > 0);
+        commit(B.k_full);
+      };
+      // scores of step n over the channels of half h
+      auto qk = [&](uint32_t n, int h, uint32_t qb) {
+        const uint64_t dQ = sw128_desc(base + G::oQ + qb * G::kQ + h * (NM * 512));
+#pragma unroll
+        for (int k = 0; k < G::CH / 8; ++k)
+          mma_tf32(tm + G::cS + (n & 1) * NM, tm + G::cK + 8 * k,
+                   dQ + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM), h > 0 || k > 0);
+      };
+      auto v_ident = [&](uint32_t n) {
+        const uint32_t op = n % G::kOps;
+        const uint32_t ob = base + G::oOp + op * G::kOp, sb = base + G::oSf + op * G::kSf + 512 * G::kAtoms;
+        const uint32_t sf = tm + G::cSfV + (n & 1) * 4 * G::kAtoms;
+        for (int at = 0; at < G::kAtoms; ++at) cp_sf(sf + 4 * at, sf_desc(sb + 512 * at));
+#pragma unroll
+        for (int h = 0; h < G::kHalves; ++h) {
+          const uint64_t dV = sw128_desc(ob + (D == 256 ? 16384 + 64 * h : 64));
+          const uint32_t d = tm + G::cV + (D == 256 ? 128 * h : 128 * (int)(n & 1));
+#pragma unroll
+          for (int k = 0; k < G::CH / 64; ++k)
+            mma_mxf4(d, dI + (uint64_t)(2 * k), dV + (uint64_t)(2 * k), idesc_mxf4(128, 2 * k), tm + G::cSfI,
+                     sf + 4 * h, k > 0);
+        }
+        commit(B.v_full + (n & 1));
+        commit(B.op_empty + op);
+      };
+      auto pv = [&](uint32_t n) {
+        wait(B.p_full + (n & 1), n >> 1);
+        wait(B.v_full + (n & 1), n >> 1);
+        fence_after();
+        const uint64_t dP = sw128_desc(base + G::oP + (n & 1) * G::kP);
+        const uint32_t keep = firsts >> (n & 1) & 1 ? 0u : 1u;
+#pragma unroll
+        for (int h = 0; h < G::kHalves; ++h)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            mma_tf32(tm + G::cO + h * NM, tm + G::cV + (D == 256 ? 128 * h : 128 * (int)(n & 1)) + 8 * k,
+                     dP + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM), k > 0 ? 1u : keep);
+        commit(B.pv + (n & 1));
+      };
+      if (u0 < u1) k_ident(0, 0);
+      int r = r0;
+      for (uint32_t u = u0; u < u1; ++seg) {
+        const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+        r = s.r;
+        u += (uint32_t)(s.k1 - s.k0);
+        const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
+        const uint32_t qb = seg % G::kQs;
+        wait(B.q_full + qb, seg / G::kQs);
+        for (int st = 0; st < steps; ++st, ++i) {
+          if (dead()) break;
+          const bool next = st + 1 < steps || u < u1;
+          if constexpr (D == 256) {
+            wait(B.k_full, kc++);
+            fence_after();
+            qk(i, 0, qb);
+            commit(B.half);
+            wait(B.half, i);
+            k_ident(i, 1);
+            if (i >= 1) pv(i - 1);
+            wait(B.k_full, kc++);
+            fence_after();
+            qk(i, 1, qb);
+            commit(B.s_full + (i & 1));
+            if (st + 1 == steps) commit(B.q_empty + qb);
+            firsts = (firsts & ~(1u << (i & 1))) | (uint32_t)(st == 0) << (i & 1);
+            if (next) {
+              wait(B.s_full + (i & 1), i >> 1);
+              k_ident(i + 1, 0);
+            }
+            if (i >= 1) wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
+            v_ident(i);
+          } else {
+            if (i >= 2) wait(B.p_full + (i & 1), (i - 2) >> 1);  // the scores two steps ago are read
+            wait(B.k_full, kc++);
+            fence_after();
+            qk(i, 0, qb);
+            commit(B.s_full + (i & 1));
+            if (st + 1 == steps) commit(B.q_empty + qb);
+            if (i >= 2) pv(i - 2);
+            firsts = (firsts & ~(1u << (i & 1))) | (uint32_t)(st == 0) << (i & 1);
+            if (next) {
+              wait(B.s_full + (i & 1), i >> 1);  // the keys of this step are used up
+              k_ident(i + 1, 0);
+            }
+            if (i >= 2) wait(B.pv + (i & 1), (i - 2) >> 1);
+            v_ident(i);
+          }
+        }
+        if (dead()) break;
+      }
+      if (!dead()) {
+        if (D != 256 && i >= 2) pv(i - 2);
+        if (i >= 1) pv(i - 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp < kLayWarp) {
+    // -------------------------------------------------------------- the softmax, the output ----
+    const int quad = warp & 3;                       // tensor-memory lanes 32 quad ..
+    const uint32_t tl = tm + ((uint32_t)quad << 21);  // (lane in bits 16..)
+    const int tok = 32 * quad + lane;                // this thread's token of a step
+    uint32_t i = 0;
+    int r = r0;
+    for (uint32_t u = u0; u < u1;) {
+      const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+      r = s.r;
+      const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first), row0 = starts[s.r];
+      const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
+      if (quad == 0 && lane < RN) {
+        mref[lane] = kLow;
+        rowpos[lane] = lane < nrow ? s.q.L - s.q.nq + (first + lane) / a.G : INT32_MIN / 2;
+        nanrow[lane] = 0;
+      }
+      soft_sync();
+      float l[RN];
+#pragma unroll
+      for (int k = 0; k < RN; ++k) l[k] = 0.f;
+      for (int st = 0; st < steps; ++st, ++i) {
+        const uint32_t b = i & 1;
+        const Info& inf = infos[i % kInfos];
+        wait(B.info + i % kInfos, i / kInfos);
+        const uint32_t fl = inf.flags[tok];
+        const bool full = inf.full != 0;
+        const int t0 = inf.t0[tok >> 4], t = t0 < 0 ? INT32_MAX : t0 + (tok & 15);
+        wait(B.s_full + b, i >> 1);
+        fence_after();
+        float x[RN];
+        tmem_ld<RN>(tl + G::cS + b * NM, x);
+        uint32_t seen = ~0u;
+        if (!full) {
+          seen = 0;
+#pragma unroll
+          for (int k = 0; k < RN; ++k) {
+            const int p = rowpos[k];
+            if (t <= p && (a.window == 0 || t > p - a.window || t < a.sinks)) seen |= 1u << k;
+          }
+        }
+        if (__any_sync(~0u, fl != 0)) {  // NaN scales
+#pragma unroll
+          for (int k = 0; k < RN; ++k) {
+            if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);
+            if ((fl & 255u) && (seen >> k & 1)) atomicOr(nanrow + k, fl & 255u);
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < RN; ++k) {
+          if (!full && !(seen >> k & 1)) x[k] = -INFINITY;
+          x[k] = fmaf(x[k], a.scale_log2, -mref[k]);
+          top = fmaxf(top, x[k]);
+        }
+        if (soft_any(top > kOver)) {
+          // the rows' references move to the maxima over this step's 128 tokens (from the scores
+          // themselves: against the initial reference x has lost them)
+          tmem_ld<RN>(tl + G::cS + b * NM, x);
+#pragma unroll
+          for (int k = 0; k < RN; ++k) {
+            if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);
+            x[k] = (seen >> k & 1) ? x[k] * a.scale_log2 : -INFINITY;
+          }
+          {
+            float y[RN];
+#pragma unroll
+            for (int k = 0; k < RN; ++k) y[k] = x[k];
+            const float w = warp_max_of<RN>(y);
+            if (lane < RN) red[quad * RN + lane] = w;
+          }
+          soft_sync();
+          float f[RN];
+#pragma unroll
+          for (int k = 0; k < RN; ++k) {
+            const float d = fmaxf(fmaxf(red[k], red[RN + k]), fmaxf(red[2 * RN + k], red[3 * RN + k]));
+            const float old = mref[k], m = fmaxf(old, d);
+            x[k] -= m;
+            f[k] = ex2(old - m);
+            l[k] *= f[k];
+          }
+          soft_sync();
+          if (quad == 0 && lane < RN)
+            mref[lane] = fmaxf(mref[lane], fmaxf(fmaxf(red[lane], red[RN + lane]), fmaxf(red[2 * RN + lane], red[3 * RN + lane])));
+          soft_sync();  // (red is free again)
+          if (st > 0) {
+            // the sums so far, once no product adds to them
+            wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
+            fence_after();
+#pragma unroll
+            for (int h = 0; h < G::kHalves; ++h) {
+              float o[RN];
+              tmem_ld<RN>(tl + G::cO + h * NM, o);
+#pragma unroll
+              for (int k = 0; k < RN; ++k) o[k] *= f[k];
+              tmem_st<RN>(tl + G::cO + h * NM, o);
+            }
+          }
+        }
+        if (i >= 2) wait(B.pv + b, (i - 2) >> 1);  // the product has read the numerators before these
+        uint8_t* ps = sm + G::oP + b * G::kP + quad * (NM * 128) + (lane & 3) * 4;
+#pragma unroll
+        for (int k = 0; k < RN; ++k) {
+          const float p = to_tf32(ex2(x[k]));
+          l[k] += p;
+          *reinterpret_cast<float*>(ps + k * 128 + (((lane >> 2) ^ (k & 7)) << 4)) = p;
+        }
+        fence_proxy();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.p_full + b);
+      }
+
+      // ---- the part's sums and averages
+      const float lw = warp_sum_of<RN>(l);
+      if (lane < RN) lsum[quad * RN + lane] = lw;
+      wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
+      fence_after();
+      soft_sync();
+      const bool whole = s.k0 == 0 && s.k1 == s.q.n;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (s.k0 == 0 ? 1 : 0);
+      float* po = a.part + slot * RN * D;
+      float* pml = a.part + 2 * (int64_t)a.ctas * RN * D + slot * RN * 2;
+#pragma unroll
+      for (int h = 0; h < G::kHalves; ++h) {
+        float o[RN];
+        tmem_ld<RN>(tl + G::cO + h * NM, o);
+        const int ch = 128 * h + tok;  // (D 64: the upper lanes hold zeros)
+        if (tok < G::CH) {
+#pragma unroll
+          for (int k = 0; k < RN; ++k) {
+            if (k < nrow) {
+              const float sum = (lsum[k] + lsum[RN + k]) + (lsum[2 * RN + k] + lsum[3 * RN + k]);
+              float v = sum == 0.f ? 0.f : o[k] / sum;
+              if (nanrow[k] >> (ch >> 5) & 1) v = __uint_as_float(0x7FC00000u);
+              if (whole) {
+                const int rho = first + k, tk = rho / a.G;
+                a.out[(row0 + tk) * a.ldo + (int64_t)(s.h * a.G + rho - tk * a.G) * D + ch] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(v));
+              } else {
+                po[k * D + ch] = v;
+                if (h == 0 && tok == 0) *reinterpret_cast<float2*>(pml + 2 * k) = make_float2(mref[k], sum);
+              }
+            }
+          }
+        }
+      }
+      u += (uint32_t)(s.k1 - s.k0);
+      if (u >= u1 && quad == 0 && lane == 0) {
+        JoinRec rec;
+        rec.last = s.k0 == 0 && !whole ? (int)((s.item + (uint32_t)s.q.n - 1) / per) : -1;
+        rec.row0 = row0, rec.first = first, rec.head = s.h, rec.rows = nrow;
+        rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
+        recs[blockIdx.x] = rec;
+      }
+      fence_before();
+      soft_sync();  // (the next part's notes overwrite these)
+    }
+  } else {
+    // ----------------------------------------- cached bytes into the tensor cores' operands ----
+    const int j = warp - kLayWarp, g = lane >> 2, c = lane & 3;
+    uint32_t i = 0, seg = 0;
+    int r = r0;
+    for (uint32_t u = u0; u < u1; ++seg) {
+      const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+      r = s.r;
+      const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first), row0 = starts[s.r];
+      const int pmax = s.q.L - s.q.nq + (first + nrow - 1) / a.G;
+      const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
+      // the item's queries: bf16 to tf32, rows of 32 channels
+      {
+        const uint32_t qb = seg % G::kQs;
+        if (seg >= (uint32_t)G::kQs) wait(B.q_empty + qb, seg / G::kQs - 1);
+        uint8_t* dst = sm + G::oQ + qb * G::kQ;
+#pragma unroll
+        for (int rr = 0; rr < (NM + 7) / 8; ++rr) {
+          const int k = j + 8 * rr;
+          if (k < NM) {
+            const int rho = first + k, tk = rho / a.G;
+            const uint16_t* p = a.q + (row0 + tk) * a.ldq + (int64_t)(s.h * a.G + rho - tk * a.G) * D;
+#pragma unroll
+            for (int e = 0; e < (D + 127) / 128; ++e) {
+              const int ch = 128 * e + 4 * lane;
+              if (ch < D) {
+                uint2 v = make_uint2(0, 0);
+                if (k < nrow) v = *reinterpret_cast<const uint2*>(p + ch);
+                *reinterpret_cast<uint4*>(dst + (ch >> 5) * (NM * 128) + k * 128 + ((((ch & 31) >> 2) ^ (k & 7)) << 4)) =
+                    make_uint4(v.x << 16, v.x & 0xFFFF0000u, v.y << 16, v.y & 0xFFFF0000u);
+              }
+            }
+          }
+        }
+        fence_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.q_full + qb);
+      }
+      for (int st = 0; st < steps; ++st, ++i) {
+        const uint32_t rs = i % G::kRaw, op = i % G::kOps;
+        if (i >= (uint32_t)G::kOps) wait(B.op_empty + op, i / G::kOps - 1);
+        wait(B.raw_full + rs, i / G::kRaw);
+        const uint8_t* tp = sm + G::oRaw + rs * G::kStep + j * G::kTile;
+        uint8_t* ob = sm + G::oOp + op * G::kOp;
+        uint8_t* sb = sm + G::oSf + op * G::kSf;
+        const int t0 = raw_info[rs * 12 + j], full = raw_info[rs * 12 + 8];
+        // keys: lane (g, c) holds 8 channels of each block of tokens g and g + 8
+        uint32_t kw[D / 16], vw[D / 16];
+#pragma unroll
+        for (int v = 0; v < D / 64; ++v) {
+          const uint4 x = *reinterpret_cast<const uint4*>(tp + v * 512 + lane * 16);
+          kw[4 * v] = x.x, kw[4 * v + 1] = x.y, kw[4 * v + 2] = x.z, kw[4 * v + 3] = x.w;
+        }
+        // values: a transposing load turns the pieces of lanes g = 0..7 into 4 bytes of a row each
+#pragma unroll
+        for (int v = 0; v < D / 64; ++v) {
+          const uint32_t ad = smem_u32(tp + 8 * D + v * 512 + ((lane & 7) * 4 + (lane >> 3)) * 16);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(vw[4 * v]), "=r"(vw[4 * v + 1]), "=r"(vw[4 * v + 2]), "=r"(vw[4 * v + 3])
+                       : "r"(ad));
+        }
+        // scales: lanes 0..15 a token's of its keys, lanes 16..31 of its values
+        const int t = lane & 15;
+        uint32_t sw[G::kAtoms];
+        if (lane < 16) {
+          const uint8_t* p = tp + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
+          if constexpr (NB == 2) sw[0] = *reinterpret_cast<const uint16_t*>(p);
+          else
+#pragma unroll
+            for (int at = 0; at < G::kAtoms; ++at) sw[at] = reinterpret_cast<const uint32_t*>(p)[at];
+        } else {
+          const uint8_t* p = tp + 16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + (t >> 3) * 2 + (t & 1);
+#pragma unroll
+          for (int at = 0; at < G::kAtoms; ++at) {
+            sw[at] = 0;
+#pragma unroll
+            for (int b = 0; b < (NB < 4 ? NB : 4); ++b) sw[at] |= (uint32_t)p[16 * at + 4 * b] << (8 * b);
+          }
+        }
+        const bool unseen = t0 < 0 || t0 + t > pmax;
+        uint32_t fl = 0;
+#pragma unroll
+        for (int at = 0; at < G::kAtoms; ++at) {
+          const uint32_t nan = unseen ? 0u : ff_bytes(sw[at]);
+          fl |= nan << (4 * at);
+          // a token that no row sees, or a NaN scale (reported in the flags): zero
+          if (unseen) sw[at] = 0;
+          else if (nan) sw[at] &= ~(((nan & 1) * 0xFFu) | ((nan >> 1 & 1) * 0xFF00u) | ((nan >> 2 & 1) * 0xFF0000u) |
+                                    ((nan >> 3 & 1) * 0xFF000000u));
+        }
+        const uint32_t kfl = __shfl_sync(~0u, fl, t);           // of the token's keys
+        const uint32_t vfl = __shfl_sync(~0u, fl, 16 + t);      // and values
+        // stores
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+          const int hh = w / NB, b = w % NB;
+          *reinterpret_cast<uint32_t*>(ob + (16 * j + 8 * hh + g) * 128 + ((b ^ g) << 4) + 4 * c) = kw[w];
+        }
+#pragma unroll
+        for (int v = 0; v < D / 64; ++v) {
+          const int piece = 8 * v + (lane >> 2), ho = piece / NB, b = piece % NB;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            const int tt = 8 * (ho >> 1) + 2 * cc + (ho & 1);
+            uint8_t* row = ob + (D == 256 ? 16384 : 0) + (16 * j + tt) * 128;
+            *reinterpret_cast<uint32_t*>(row + (((D == 256 ? b : 4 + b) ^ (tt & 7)) << 4) + 4 * c) = vw[4 * v + cc];
+          }
+        }
+        const int mrow = 16 * j + t;
+#pragma unroll
+        for (int at = 0; at < G::kAtoms; ++at)
+          *reinterpret_cast<uint32_t*>(sb + (lane < 16 ? 0 : 512 * G::kAtoms) + 512 * at + 16 * (mrow & 31) + 4 * (mrow >> 5)) = sw[at];
+        Info& inf = infos[i % kInfos];
+        if (lane < 16) inf.flags[mrow] = (uint16_t)((kfl ? 0x8000u : 0u) | vfl);
+        if (lane == 16) inf.t0[j] = t0;
+        if (lane == 17 && j == 0) inf.full = full;
+        fence_proxy();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(B.raw_empty + rs);
+          mbar_arrive(B.info + i % kInfos);
+          mbar_arrive(B.op_full + op);
+        }
+      }
+      u += (uint32_t)(s.k1 - s.k0);
+    }
+  }
+
+  if (dead()) {  // let the copies and products in flight end before their memory goes
+    const int64_t t0 = clock64();
+    while (clock64() - t0 < 2000000) __nanosleep(1000);
+  }
+  fence_before();
+  __syncthreads();
+  mtail::pdl_trigger();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+}
+
+// Joins the parts of the items that several ranges share.  CTA (x, y): the item that crosses the
+// end of range x for the first time, rows 4 y .. 4 y + 3, one per warp:
+//   out = sum_k w_k o_k / sum_k w_k,  w_k = l_k 2^(m_k - max m), in range order.
+template <int D>
+__global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ AttnArgs a, int rn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  mtail::pdl_wait();
+  const JoinRec rec = reinterpret_cast<const JoinRec*>(a.part + 2 * (int64_t)a.ctas * rn * (D + 2))[blockIdx.x];
+  const int i = blockIdx.y * 4 + warp;
+  if (rec.last < 0 || i >= rec.rows) return;
+  const int c0 = blockIdx.x, c1 = rec.last;
+  const float* po = a.part + (int64_t)i * D;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + 2 * (int64_t)a.ctas * rn * D) + i;
+  auto slot = [&](int k) { return 2 * (int64_t)k + (k == c0 ? 1 : 0); };
+  float m = kLow;
+  for (int k = c0 + lane; k <= c1; k += 32) m = fmaxf(m, ml[slot(k) * rn].x);
+  m = mtail::warp_max(m);
+  m = __shfl_sync(~0u, m, 0);
+  constexpr int E = D / 32;
+  float o[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 8
+  for (int k = c0; k <= c1; ++k) {
+    const float2 v = ml[slot(k) * rn];
+    const float w = v.y * ex2(v.x - m);
+    const float* p = po + slot(k) * rn * D + lane * E;
+    sum += w;
+    if constexpr (E == 2) {
+      const float2 x = *reinterpret_cast<const float2*>(p);
+      o[0] = fmaf(w, x.x, o[0]), o[1] = fmaf(w, x.y, o[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + e);
+        o[e] = fmaf(w, x.x, o[e]), o[e + 1] = fmaf(w, x.y, o[e + 1]);
+        o[e + 2] = fmaf(w, x.z, o[e + 2]), o[e + 3] = fmaf(w, x.w, o[e + 3]);
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int rho = rec.first + i, tok = rho / a.G;
+  uint16_t* orow = a.out + (rec.row0 + tok) * a.ldo + (int64_t)(rec.head * a.G + rho - tok * a.G) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    reinterpret_cast<uint32_t*>(orow)[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+template <int D, int RN>
+cudaError_t prepare() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // once per device (racing threads do the same)
+  static std::atomic<int> known[64];
+  if (dev < 64 && known[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(k_kv4_attn<D, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Geo<D, RN>::smem(kMaxReqs));
+  if (e == cudaSuccess && dev < 64) known[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+template <int D, int RN>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  static_assert(Geo<D, RN>::smem(kMaxReqs) <= 232448 - 256, "shared memory");
+  cudaError_t e = prepare<D, RN>();
+  if (e != cudaSuccess) return e;
+  k_kv4_attn<D, RN><<<a.ctas, kThreads, Geo<D, RN>::smem(a.reqs), st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.ctas < 2) return e;
+  return mtail::launch_k(k_kv4_join<D>, dim3(a.ctas - 1, RN / 4), dim3(128), 0, st, true, a, RN);
+}
+
+template <typename F>
+cudaError_t dispatch(int D, int rn, F&& f) {
+  switch (D * 100 + rn) {
+    case 6408: return f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+    case 6416: return f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+    case 6432: return f(std::integral_constant<int, 64>(), std::integral_constant<int, 32>());
+    case 12808: return f(std::integral_constant<int, 128>(), std::integral_constant<int, 8>());
+    case 12816: return f(std::integral_constant<int, 128>(), std::integral_constant<int, 16>());
+    case 12832: return f(std::integral_constant<int, 128>(), std::integral_constant<int, 32>());
+    case 25608: return f(std::integral_constant<int, 256>(), std::integral_constant<int, 8>());
+    case 25616: return f(std::integral_constant<int, 256>(), std::integral_constant<int, 16>());
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+int attn_rows_per_item(int D, int G, int max_new) {
+  const int64_t rows = (int64_t)G * max_new;
+  return rows <= 8 ? 8 : (rows <= 16 || D == 256) ? 16 : 32;
+}
+
+int attn_ctas(int D, int rn, cudaError_t* err) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  *err = e;
+  return e == cudaSuccess ? sms : 0;
+}
+
+size_t attn_workspace_bytes(int D, int rn, int ctas) {
+  return (size_t)2 * ctas * rn * (D + 2) * sizeof(float) + (size_t)ctas * sizeof(JoinRec);
+}
+
+cudaError_t launch_kv4_attention(const AttnArgs& a, int rn, cudaStream_t st) {
+  return dispatch(a.D, rn, [&](auto d, auto n) { return launch<decltype(d)::value, decltype(n)::value>(a, st); });
+}
+
+}  // namespace kv4
