@@ -48,26 +48,35 @@ using mtail::bulk_load;
 using mtail::mbar_arrive;
 using mtail::mbar_expect_tx;
 using mtail::mbar_init;
-using mtail::mbar_try_wait;
 using mtail::smem_u32;
 
 namespace {
 
-constexpr int kWarps = 14, kThreads = 32 * kWarps;
-constexpr int kLayWarp = 6;  // (0 copies, 1 products, 2..5 softmax)
+// warps: 0 copies, 1 key products, 2..5 and 15..18 softmax (rows of the lower and the upper half;
+// warp mod 4 = the tensor-memory lanes it reaches), 6..13 layout, 14 value products
+constexpr int kWarps = 19, kThreads = 32 * kWarps;
+constexpr int kLayWarp = 6, kValWarp = 14, kSoft2Warp = 15;
 constexpr int kStepTiles = 8;
 constexpr int kInfos = 8;                     // steps whose notes are kept
 constexpr int64_t kBudgetClocks = 200000000;  // of a wait, about 0.1 s
 constexpr float kLow = -3.0e38f;              // a row's reference before its first score
 constexpr float kOver = 40.f;                 // octaves above the reference that move it
-constexpr uint32_t kBarSoft = 1;              // named barrier of the softmax warps
+
+// A position in a ring of N buffers and the parity of its pass.
+template <int N>
+struct Ring {
+  uint32_t i = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) i = 0, ph ^= 1;
+  }
+};
 
 // What the softmax needs to know of a step's tokens.
 struct Info {
-  int t0[kStepTiles];     // first token of each tile, negative: the tile has no page
+  uint64_t plain;         // byte j is 1: every row sees all of tile j, no scale of it is a NaN
+  // of the other tiles:
+  int t0[kStepTiles];     // their first token, negative: the tile has no page
   uint16_t flags[128];    // of a token: bit 15 a NaN among its key scales, bit b one at value block b
-  int full;               // every row sees every token
-  int pad[3];
 };
 
 template <int D, int RN>
@@ -86,18 +95,18 @@ struct Geo {
   static constexpr int kSf = 2 * kAtoms * 512;           // key atoms, then value atoms
   static constexpr int kP = NM * 512, kQ = NM * D * 4;
   // tensor-memory columns
-  static constexpr int cK = 0, cV = 128, cS = 384, cO = cS + 2 * NM;
-  static constexpr int cSfK = cO + kHalves * NM, cSfV = cSfK + 8 * kAtoms, cSfI = cSfV + 8 * kAtoms;
-  static_assert(cSfI + 4 <= 512, "tensor memory");
+  static constexpr int cK = 0, cV = 256, cS = 384, cO = cS + 2 * NM;  // (K' twice, V' once)
+  static constexpr int cSfK = cO + kHalves * NM, cSfV = cSfK + 8 * kAtoms, cSfI = cSfV + 4 * kAtoms, cSfJ = cSfI + 4;
+  static_assert(cSfJ + 4 <= 512, "tensor memory");
   // shared memory (from a 1024-byte boundary)
   static constexpr int oOp = 0, oI = oOp + kOps * kOp, oQ = oI + 16384, oP = oQ + kQs * kQ;
   static constexpr int oRaw = oP + 2 * kP, oSf = (oRaw + kRaw * kStep + 127) / 128 * 128;
   static constexpr int oSfI = oSf + kOps * kSf, oInfo = oSfI + 512;
   static constexpr int oSmall = oInfo + kInfos * (int)sizeof(Info);
   // raw and operand rings, info ring, q, and the single ones
-  static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 10;
-  static constexpr int kSmall = kBars * 8 + kRaw * 12 * 4 /* t0, full */ + 4 * RN * 8 /* red, l */ +
-                                RN * 12 /* references, rowpos, nan */ + 64;
+  static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 12 + 4;
+  static constexpr int kSmall = kBars * 8 + kRaw * 20 * 4 /* t0, full */ + 4 * RN * 8 /* red, l */ +
+                                RN * 8 /* rowpos, nan */ + 64 + 32 /* over */;
   static constexpr size_t smem(int reqs) {
     return 1024 + (size_t)oSmall + kSmall + (size_t)(3 * reqs + 2) * 4;
   }
@@ -162,11 +171,22 @@ __device__ __forceinline__ void st8(uint32_t t, const uint32_t* r) {
 }
 #undef KV4_R8
 #undef KV4_W8
+__device__ __forceinline__ void ld4(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(t));
+}
+__device__ __forceinline__ void st4(uint32_t t, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
+}
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[N]) {
   uint32_t r[N];
 #pragma unroll
-  for (int i = 0; i < N; i += 8) ld8(t + i, r + i);
+  for (int i = 0; i < N; i += 8) {
+    if (N % 8) ld4(t + i, r + i);
+    else ld8(t + i, r + i);
+  }
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
@@ -177,7 +197,10 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = __float_as_uint(v[i]);
 #pragma unroll
-  for (int i = 0; i < N; i += 8) st8(t + i, r + i);
+  for (int i = 0; i < N; i += 8) {
+    if (N % 8) st4(t + i, r + i);
+    else st8(t + i, r + i);
+  }
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -185,21 +208,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// to the nearest tf32 (a NaN may come out as a zero)
 __device__ __forceinline__ float to_tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return __uint_as_float(r);
+  return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xFFFFE000u);
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync %0, 128;" ::"n"(kBarSoft) : "memory"); }
-__device__ __forceinline__ bool soft_any(bool p) {
-  uint32_t r;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
-      : "=r"(r)
-      : "r"((uint32_t)p), "n"(kBarSoft)
-      : "memory");
-  return r != 0;
-}
+// the four softmax warps of one half of the rows
+__device__ __forceinline__ void soft_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 // bytes of w that are 255, one bit each
 __device__ __forceinline__ uint32_t ff_bytes(uint32_t w) {
   const uint32_t f = ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
@@ -240,9 +254,30 @@ __device__ __forceinline__ float warp_sum_of(float (&v)[N]) {
   return v[0];
 }
 
+// Waits in hardware for up to 0.2 ms (without the hint a waiting warp polls, and a dozen of them
+// take the shared-memory pipe from the others).
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity), "r"(200000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 struct Bars {
   uint64_t *raw_full, *raw_empty, *op_full, *op_empty, *info, *q_full, *q_empty;
-  uint64_t *k_full, *half, *s_full, *p_full, *v_full, *pv;  // half: QK of the first half done
+  uint64_t *k_full, *k_free, *s_full, *p_full, *v_full, *v_free, *pv, *soft;
 };
 
 // The record that tells the joining launch which item crosses the end of a range.
@@ -275,16 +310,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   B.q_full = B.info + kInfos;
   B.q_empty = B.q_full + 2;
   B.k_full = B.q_empty + 2;
-  B.half = B.k_full + 1;
-  B.s_full = B.half + 1;
+  B.s_full = B.k_full + 4;
+  B.k_free = G::kHalves > 1 ? B.k_full + 2 : B.s_full;  // (one half: the scores are all that use them)
   B.p_full = B.s_full + 2;
   B.v_full = B.p_full + 2;
-  B.pv = B.v_full + 2;
-  int* raw_info = reinterpret_cast<int*>(bp + G::kBars);  // [kRaw][12]: t0 of the tiles, full
-  float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 12);  // [4][RN]
+  B.v_free = B.v_full + 1;
+  B.pv = B.v_free + 1;
+  B.soft = B.pv + 2;
+  int* raw_info = reinterpret_cast<int*>(bp + G::kBars);  // [kRaw][20]: t0 of the tiles, full
+  float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 20);  // [4][RN]
   float* lsum = red + 4 * RN;                                       // [4][RN]
-  float* mref = lsum + 4 * RN;                                      // [RN]
-  int* rowpos = reinterpret_cast<int*>(mref + RN);
+  int* rowpos = reinterpret_cast<int*>(lsum + 4 * RN);
   uint32_t* nanrow = reinterpret_cast<uint32_t*>(rowpos + RN);
   uint32_t* pre = nanrow + RN + 16;
   int* lens = reinterpret_cast<int*>(pre + a.reqs + 1);
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     for (int i = 0; i < G::kBars; ++i) {
       uint64_t* b = bp + i;
       const bool lay = (b >= B.raw_empty && b < B.op_empty) || (b >= B.info && b < B.q_empty);
-      mbar_init(b, lay ? 8u : b >= B.p_full && b < B.v_full ? 4u : 1u);
+      mbar_init(b, lay ? 8u : b >= B.op_empty && b < B.info ? 2u : b >= B.p_full && b < B.v_full ? 8u : b >= B.soft ? 4u : 1u);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -327,31 +363,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = s_tmem;
+  const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
   const uint32_t u0 = (uint32_t)min(u0w, (uint64_t)total), u1 = min(total, u0 + per);
   if (u0 == u1 && tid == 0) recs[blockIdx.x].last = -1;
 
+  bool gone = false;  // a wait gave up, here or elsewhere in the CTA
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (mbar_try_wait(b, parity & 1)) return;
+    if (mbar_sleep_wait(b, parity & 1)) return;
     const int64_t t0 = clock64();
-    for (;;) {
-#pragma unroll 1
-      for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(b, parity & 1)) return;
-      if (*reinterpret_cast<volatile int*>(&s_dead)) return;
-      if (clock64() - t0 > kBudgetClocks) {
+    while (!mbar_sleep_wait(b, parity & 1)) {
+      gone = *reinterpret_cast<volatile int*>(&s_dead) != 0;
+      if (!gone && clock64() - t0 > kBudgetClocks) {
+        gone = true;
         *reinterpret_cast<volatile int*>(&s_dead) = 1;
         if (a.status) atomicOr(a.status, kStatusTimeout);
-        return;
       }
+      if (gone) return;
     }
   };
-  auto dead = [&]() { return *reinterpret_cast<volatile int*>(&s_dead) != 0; };
   const int r0 = u0 < u1 ? find_req(pre, a.reqs, u0) : 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ the tiles' copies ----
-    uint32_t i = 0;
+    Ring<G::kRaw> raw;
     int r = r0;
     for (uint32_t u = u0; u < u1;) {
       const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
@@ -372,18 +406,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         }
         const int t0 = tile * 16;
         const bool full = at >= 0 && t0 + 15 <= pmin && (a.window == 0 || t0 > pmax - a.window || t0 + 15 < a.sinks);
-        const uint32_t have = __ballot_sync(~0u, at >= 0), fulls = __ballot_sync(~0u, full);
+        const uint32_t have = __ballot_sync(~0u, at >= 0);
         const int steps = (min(32, s.k1 - k) + kStepTiles - 1) / kStepTiles;
-        for (int q = 0; q < steps; ++q, ++i) {
-          const int st = (int)(i % G::kRaw);
-          const uint32_t n = i / G::kRaw;
-          if (n > 0) wait(B.raw_empty + st, n - 1);
+        for (int q = 0; q < steps; ++q, raw.next()) {
+          const uint32_t st = raw.i;
+          wait(B.raw_empty + st, raw.ph ^ 1);
           uint8_t* dst = sm + G::oRaw + st * G::kStep;
           const uint32_t mine = have >> (8 * q) & 255;
-          if (lane >> 3 == q) raw_info[st * 12 + (lane & 7)] = at >= 0 ? t0 : -1;
-          if (lane == 0) raw_info[st * 12 + 8] = (fulls >> (8 * q) & 255) == 255;
+          if (lane >> 3 == q) raw_info[st * 20 + (lane & 7)] = at >= 0 ? t0 : -1, raw_info[st * 20 + 8 + (lane & 7)] = full;
           __syncwarp();
-          const bool go = !dead();
+          const bool go = !__any_sync(~0u, gone);
           if (lane == 0) {
             if (mine && go) mbar_expect_tx(B.raw_full + st, __popc(mine) * G::kTile);
             else mbar_arrive(B.raw_full + st);
@@ -396,131 +428,149 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       u += (uint32_t)(s.k1 - s.k0);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------- the tensor cores ----
-    if (elect_one()) {
-      const uint32_t base = smem_u32(sm);
-      const uint64_t dI = sw128_desc(base + G::oI);
-      cp_sf(tm + G::cSfI, sf_desc(base + G::oSfI));
-      uint32_t i = 0, seg = 0, kc = 0;
-      uint32_t firsts = 0;  // bit n & 1: step n began an item's part
-      // dequantised keys of step n, half h (its operands waited for with the first half)
-      auto k_ident = [&](uint32_t n, int h) {
-        const uint32_t op = n % G::kOps;
-        const uint32_t ob = base + G::oOp + op * G::kOp, sb = base + G::oSf + op * G::kSf;
+    // --------------------------------------- the tensor cores: K' = K I, S^T = K' Q^T ----
+    // The warp stays together; each run of products is one elected thread's (the same every time),
+    // whose operands the compiler then keeps in uniform registers: 9 cycles an instruction instead
+    // of 46 from a divergent thread.  Sub-step n is half n % kHalves (of the channels) of step n /
+    // kHalves; the dequantised keys of the next one are asked for before the scores of this one,
+    // where its operands are there.
+    const uint32_t base = smem_u32(sm);
+    const uint64_t dI = sw128_desc(base + G::oI);
+    if (elect_one()) cp_sf(tm + G::cSfI, sf_desc(base + G::oSfI));
+    __syncwarp();
+    Ring<G::kOps> ahead;  // the operands of the next sub-step whose keys are asked for
+    auto k_ident = [&](uint32_t n) {
+      const uint32_t h = n % G::kHalves, nb = n & 1;
+      const uint32_t ob = base + G::oOp + ahead.i * G::kOp, sb = base + G::oSf + ahead.i * G::kSf;
+      const uint32_t sf = tm + G::cSfK + (n / G::kHalves & 1) * 4 * G::kAtoms;
+      if (h == 0) wait(B.op_full + ahead.i, ahead.ph);
+      wait(B.k_free + nb, (n >> 1) + 1);  // the scores two sub-steps ago
+      fence_after();
+      if (elect_one()) {
         if (h == 0) {
-          wait(B.op_full + op, n / G::kOps);
-          fence_after();
-          for (int at = 0; at < G::kAtoms; ++at)
-            cp_sf(tm + G::cSfK + (n & 1) * 4 * G::kAtoms + 4 * at, sf_desc(sb + 512 * at));
+#pragma unroll
+          for (int at = 0; at < G::kAtoms; ++at) cp_sf(sf + 4 * at, sf_desc(sb + 512 * at));
         }
-        const uint64_t dK = sw128_desc(ob);
+        const uint64_t dK = sw128_desc(ob + 64 * h);
+        const uint32_t d = tm + G::cK + 128 * nb;
 #pragma unroll
         for (int k = 0; k < G::CH / 64; ++k)
-          mma_mxf4(tm + G::cK, dK + (uint64_t)((64 * h + 32 * k) >> 4), dI + (uint64_t)(2 * k),
-                   idesc_mxf4(G::CH, 2 * k), tm + G::cSfK + (n & 1) * 4 * G::kAtoms + 4 * h, tm + G::cSfI, k > 0);
-        commit(B.k_full);
-      };
-      // scores of step n over the channels of half h
-      auto qk = [&](uint32_t n, int h, uint32_t qb) {
-        const uint64_t dQ = sw128_desc(base + G::oQ + qb * G::kQ + h * (NM * 512));
+          mma_mxf4(d, dK + (uint64_t)(2 * k), dI + (uint64_t)(2 * k), idesc_mxf4(G::CH, 2 * k), sf + 4 * h,
+                   tm + G::cSfI, k > 0);
+        commit(B.k_full + nb);
+        if (h + 1 == G::kHalves) commit(B.op_empty + ahead.i);
+      }
+      __syncwarp();
+      if (h + 1 == G::kHalves) ahead.next();
+    };
+    uint32_t n = 0;
+    Ring<G::kQs> qr;
+    int r = r0;
+    if (u0 < u1) k_ident(0);
+    for (uint32_t u = u0; u < u1; qr.next()) {
+      const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+      r = s.r;
+      u += (uint32_t)(s.k1 - s.k0);
+      const int subs = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles * G::kHalves;
+      const uint32_t q0 = base + G::oQ + qr.i * G::kQ;
+      wait(B.q_full + qr.i, qr.ph);
+      for (int st = 0; st < subs; ++st, ++n) {
+        if (__any_sync(~0u, gone)) break;
+        const uint32_t i = n / G::kHalves, h = n % G::kHalves, nb = n & 1, ib = i & 1;
+        bool next = st + 1 < subs || u < u1;
+        if (next && (h + 1 < G::kHalves || __all_sync(~0u, mbar_test(B.op_full + ahead.i, ahead.ph)))) {
+          k_ident(n + 1);
+          next = false;
+        }
+        if (h == 0) wait(B.p_full + ib, (i >> 1) + 1);  // the scores two steps ago are read
+        wait(B.k_full + nb, n >> 1);
+        fence_after();
+        if (elect_one()) {
+          const uint64_t dQ = sw128_desc(q0 + h * (NM * 512));
+          const uint32_t d = tm + G::cS + ib * NM, ak = tm + G::cK + 128 * nb;
 #pragma unroll
-        for (int k = 0; k < G::CH / 8; ++k)
-          mma_tf32(tm + G::cS + (n & 1) * NM, tm + G::cK + 8 * k,
-                   dQ + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM), h > 0 || k > 0);
-      };
-      auto v_ident = [&](uint32_t n) {
-        const uint32_t op = n % G::kOps;
-        const uint32_t ob = base + G::oOp + op * G::kOp, sb = base + G::oSf + op * G::kSf + 512 * G::kAtoms;
-        const uint32_t sf = tm + G::cSfV + (n & 1) * 4 * G::kAtoms;
-        for (int at = 0; at < G::kAtoms; ++at) cp_sf(sf + 4 * at, sf_desc(sb + 512 * at));
+          for (int k = 0; k < G::CH / 8; ++k)
+            mma_tf32(d, ak + 8 * k, dQ + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM),
+                     k > 0 ? 1u : h);
+          if (G::kHalves > 1) commit(B.k_free + nb);
+          if (h + 1 == G::kHalves) commit(B.s_full + ib);
+          if (st + 1 == subs) commit(B.q_empty + qr.i);
+        }
+        __syncwarp();
+        if (next) k_ident(n + 1);
+      }
+      if (__any_sync(~0u, gone)) break;
+    }
+  } else if (warp == kValWarp) {
+    // ------------------------------------- the tensor cores: V' = I V^T, O^T += V' P^T ----
+    const uint32_t base = smem_u32(sm);
+    const uint64_t dI = sw128_desc(base + G::oI);
+    if (elect_one()) cp_sf(tm + G::cSfJ, sf_desc(base + G::oSfI));
+    __syncwarp();
+    uint32_t n = 0;
+    Ring<G::kOps> op;
+    int r = r0;
+    for (uint32_t u = u0; u < u1;) {
+      const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+      r = s.r;
+      u += (uint32_t)(s.k1 - s.k0);
+      const int subs = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles * G::kHalves;
+      for (int st = 0; st < subs; ++st, ++n) {
+        if (__any_sync(~0u, gone)) break;
+        const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1;
+        const uint32_t ob = base + G::oOp + op.i * G::kOp, sb = base + G::oSf + op.i * G::kSf + 512 * G::kAtoms;
+        if (h == 0) wait(B.op_full + op.i, op.ph);
+        // the product that read the values before these
+        if (G::kHalves > 1) wait(B.v_free, n + 1);
+        else wait(B.pv + (ib ^ 1), ((n + 1) >> 1) + 1);
+        fence_after();
+        if (elect_one()) {
+          if (h == 0) {
 #pragma unroll
-        for (int h = 0; h < G::kHalves; ++h) {
+            for (int at = 0; at < G::kAtoms; ++at) cp_sf(tm + G::cSfV + 4 * at, sf_desc(sb + 512 * at));
+          }
           const uint64_t dV = sw128_desc(ob + (D == 256 ? 16384 + 64 * h : 64));
-          const uint32_t d = tm + G::cV + (D == 256 ? 128 * h : 128 * (int)(n & 1));
 #pragma unroll
           for (int k = 0; k < G::CH / 64; ++k)
-            mma_mxf4(d, dI + (uint64_t)(2 * k), dV + (uint64_t)(2 * k), idesc_mxf4(128, 2 * k), tm + G::cSfI,
-                     sf + 4 * h, k > 0);
+            mma_mxf4(tm + G::cV, dI + (uint64_t)(2 * k), dV + (uint64_t)(2 * k), idesc_mxf4(128, 2 * k),
+                     tm + G::cSfJ, tm + G::cSfV + 4 * h, k > 0);
+          commit(B.v_full);
+          if (h + 1 == G::kHalves) commit(B.op_empty + op.i);
         }
-        commit(B.v_full + (n & 1));
-        commit(B.op_empty + op);
-      };
-      auto pv = [&](uint32_t n) {
-        wait(B.p_full + (n & 1), n >> 1);
-        wait(B.v_full + (n & 1), n >> 1);
+        __syncwarp();
+        if (h + 1 == G::kHalves) op.next();
+        if (h == 0) wait(B.p_full + ib, i >> 1);
+        wait(B.v_full, n);
         fence_after();
-        const uint64_t dP = sw128_desc(base + G::oP + (n & 1) * G::kP);
-        const uint32_t keep = firsts >> (n & 1) & 1 ? 0u : 1u;
-#pragma unroll
-        for (int h = 0; h < G::kHalves; ++h)
+        if (elect_one()) {
+          const uint64_t dP = sw128_desc(base + G::oP + ib * G::kP);
+          const uint32_t d = tm + G::cO + h * NM, keep = st < G::kHalves ? 0u : 1u;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            mma_tf32(tm + G::cO + h * NM, tm + G::cV + (D == 256 ? 128 * h : 128 * (int)(n & 1)) + 8 * k,
-                     dP + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM), k > 0 ? 1u : keep);
-        commit(B.pv + (n & 1));
-      };
-      if (u0 < u1) k_ident(0, 0);
-      int r = r0;
-      for (uint32_t u = u0; u < u1; ++seg) {
-        const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
-        r = s.r;
-        u += (uint32_t)(s.k1 - s.k0);
-        const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
-        const uint32_t qb = seg % G::kQs;
-        wait(B.q_full + qb, seg / G::kQs);
-        for (int st = 0; st < steps; ++st, ++i) {
-          if (dead()) break;
-          const bool next = st + 1 < steps || u < u1;
-          if constexpr (D == 256) {
-            wait(B.k_full, kc++);
-            fence_after();
-            qk(i, 0, qb);
-            commit(B.half);
-            wait(B.half, i);
-            k_ident(i, 1);
-            if (i >= 1) pv(i - 1);
-            wait(B.k_full, kc++);
-            fence_after();
-            qk(i, 1, qb);
-            commit(B.s_full + (i & 1));
-            if (st + 1 == steps) commit(B.q_empty + qb);
-            firsts = (firsts & ~(1u << (i & 1))) | (uint32_t)(st == 0) << (i & 1);
-            if (next) {
-              wait(B.s_full + (i & 1), i >> 1);
-              k_ident(i + 1, 0);
-            }
-            if (i >= 1) wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
-            v_ident(i);
-          } else {
-            if (i >= 2) wait(B.p_full + (i & 1), (i - 2) >> 1);  // the scores two steps ago are read
-            wait(B.k_full, kc++);
-            fence_after();
-            qk(i, 0, qb);
-            commit(B.s_full + (i & 1));
-            if (st + 1 == steps) commit(B.q_empty + qb);
-            if (i >= 2) pv(i - 2);
-            firsts = (firsts & ~(1u << (i & 1))) | (uint32_t)(st == 0) << (i & 1);
-            if (next) {
-              wait(B.s_full + (i & 1), i >> 1);  // the keys of this step are used up
-              k_ident(i + 1, 0);
-            }
-            if (i >= 2) wait(B.pv + (i & 1), (i - 2) >> 1);
-            v_ident(i);
-          }
+            mma_tf32(d, tm + G::cV + 8 * k, dP + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4),
+                     idesc_tf32(NM), k > 0 ? 1u : keep);
+          if (G::kHalves > 1) commit(B.v_free);
+          if (h + 1 == G::kHalves) commit(B.pv + ib);
         }
-        if (dead()) break;
+        __syncwarp();
       }
-      if (!dead()) {
-        if (D != 256 && i >= 2) pv(i - 2);
-        if (i >= 1) pv(i - 1);
-      }
+      if (__any_sync(~0u, gone)) break;
     }
-    __syncwarp();
-  } else if (warp < kLayWarp) {
+  } else if (warp < kLayWarp || warp >= kSoft2Warp) {
     // -------------------------------------------------------------- the softmax, the output ----
+    constexpr int RH = RN / 2;                       // rows of this warp: half of the item's
+    const int half = warp < kLayWarp ? 0 : 1, k0 = half * RH;
     const int quad = warp & 3;                       // tensor-memory lanes 32 quad ..
     const uint32_t tl = tm + ((uint32_t)quad << 21);  // (lane in bits 16..)
     const int tok = 32 * quad + lane;                // this thread's token of a step
+    uint8_t* over = reinterpret_cast<uint8_t*>(nanrow + RN) + half * 8;  // [2][4]: a warp's x passed kOver
+    // where this token's numerators of rows k0 + k go (k and k + 8 lie 1024 bytes apart)
+    uint8_t* ps[RH < 8 ? RH : 8];
+#pragma unroll
+    for (int k = 0; k < (RH < 8 ? RH : 8); ++k)
+      ps[k] = sm + G::oP + quad * (NM * 128) + (k0 + k) * 128 + (((lane >> 2) ^ ((k0 + k) & 7)) << 4) + (lane & 3) * 4;
+    float* hred = red + half * 4 * RH;
+    float* hsum = lsum + half * 4 * RH;
     uint32_t i = 0;
     int r = r0;
     for (uint32_t u = u0; u < u1;) {
@@ -528,101 +578,104 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       r = s.r;
       const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first), row0 = starts[s.r];
       const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
-      if (quad == 0 && lane < RN) {
-        mref[lane] = kLow;
-        rowpos[lane] = lane < nrow ? s.q.L - s.q.nq + (first + lane) / a.G : INT32_MIN / 2;
-        nanrow[lane] = 0;
+      if (quad == 0 && lane < RH) {
+        const int k = k0 + lane;
+        rowpos[k] = k < nrow ? s.q.L - s.q.nq + (first + k) / a.G : INT32_MIN / 2;
+        nanrow[k] = 0;
       }
-      soft_sync();
-      float l[RN];
+      soft_sync(half);
+      float l[RH], m[RH];
 #pragma unroll
-      for (int k = 0; k < RN; ++k) l[k] = 0.f;
+      for (int k = 0; k < RH; ++k) l[k] = 0.f, m[k] = kLow;
       for (int st = 0; st < steps; ++st, ++i) {
         const uint32_t b = i & 1;
         const Info& inf = infos[i % kInfos];
-        wait(B.info + i % kInfos, i / kInfos);
-        const uint32_t fl = inf.flags[tok];
-        const bool full = inf.full != 0;
-        const int t0 = inf.t0[tok >> 4], t = t0 < 0 ? INT32_MAX : t0 + (tok & 15);
+        const uint32_t sa = tl + G::cS + b * NM + k0;
         wait(B.s_full + b, i >> 1);
+        wait(B.info + i % kInfos, i / kInfos);
         fence_after();
-        float x[RN];
-        tmem_ld<RN>(tl + G::cS + b * NM, x);
-        uint32_t seen = ~0u;
-        if (!full) {
+        float x[RH];
+        tmem_ld<RH>(sa, x);
+        uint32_t seen = ~0u, fl = 0;
+        if (inf.plain != 0x0101010101010101ull) {
+          int t0 = inf.t0[tok >> 4], t = t0 < 0 ? INT32_MAX : t0 + (tok & 15);
+          fl = inf.flags[tok];
+          if (inf.plain >> (8 * (tok >> 4)) & 1) t = INT32_MIN, fl = 0;
           seen = 0;
 #pragma unroll
-          for (int k = 0; k < RN; ++k) {
-            const int p = rowpos[k];
-            if (t <= p && (a.window == 0 || t > p - a.window || t < a.sinks)) seen |= 1u << k;
-          }
-        }
-        if (__any_sync(~0u, fl != 0)) {  // NaN scales
-#pragma unroll
-          for (int k = 0; k < RN; ++k) {
-            if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);
-            if ((fl & 255u) && (seen >> k & 1)) atomicOr(nanrow + k, fl & 255u);
+          for (int k = 0; k < RH; ++k) {
+            const int p = rowpos[k0 + k];
+            if (t == INT32_MIN || (t <= p && (a.window == 0 || t > p - a.window || t < a.sinks))) seen |= 1u << k;
+            if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);  // a NaN among the key scales
+            if (!(seen >> k & 1)) x[k] = -INFINITY;
+            if ((fl & 255u) && (seen >> k & 1)) atomicOr(nanrow + k0 + k, fl & 255u);  // value scales
           }
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < RN; ++k) {
-          if (!full && !(seen >> k & 1)) x[k] = -INFINITY;
-          x[k] = fmaf(x[k], a.scale_log2, -mref[k]);
+        for (int k = 0; k < RH; ++k) {
+          x[k] = fmaf(x[k], a.scale_log2, -m[k]);
           top = fmaxf(top, x[k]);
         }
-        if (soft_any(top > kOver)) {
+        const bool mine = __any_sync(~0u, top > kOver);
+        if (lane == 0) {
+          over[4 * b + quad] = mine;
+          mbar_arrive(B.soft + 2 * half + b);
+        }
+        wait(B.pv + b, (i >> 1) + 1);  // the product has read the numerators before these
+        const uint32_t pb = b * G::kP;
+        float p[RH];
+        auto numerators = [&]() {
+#pragma unroll
+          for (int k = 0; k < RH; ++k) {
+            p[k] = ex2(x[k]);
+            *reinterpret_cast<float*>(ps[k & 7] + pb + (k >> 3) * 1024) = to_tf32(p[k]);
+          }
+        };
+        numerators();
+        wait(B.soft + 2 * half + b, i >> 1);
+        if (*reinterpret_cast<volatile uint32_t*>(over + 4 * b)) {
           // the rows' references move to the maxima over this step's 128 tokens (from the scores
           // themselves: against the initial reference x has lost them)
-          tmem_ld<RN>(tl + G::cS + b * NM, x);
+          tmem_ld<RH>(sa, x);
+          float y[RH];
 #pragma unroll
-          for (int k = 0; k < RN; ++k) {
+          for (int k = 0; k < RH; ++k) {
             if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);
             x[k] = (seen >> k & 1) ? x[k] * a.scale_log2 : -INFINITY;
+            y[k] = x[k];
           }
-          {
-            float y[RN];
+          const float w = warp_max_of<RH>(y);
+          if (lane < RH) hred[quad * RH + lane] = w;
+          soft_sync(half);
+          float f[RH];
 #pragma unroll
-            for (int k = 0; k < RN; ++k) y[k] = x[k];
-            const float w = warp_max_of<RN>(y);
-            if (lane < RN) red[quad * RN + lane] = w;
-          }
-          soft_sync();
-          float f[RN];
-#pragma unroll
-          for (int k = 0; k < RN; ++k) {
-            const float d = fmaxf(fmaxf(red[k], red[RN + k]), fmaxf(red[2 * RN + k], red[3 * RN + k]));
-            const float old = mref[k], m = fmaxf(old, d);
-            x[k] -= m;
-            f[k] = ex2(old - m);
+          for (int k = 0; k < RH; ++k) {
+            const float d = fmaxf(fmaxf(hred[k], hred[RH + k]), fmaxf(hred[2 * RH + k], hred[3 * RH + k]));
+            const float old = m[k];
+            m[k] = fmaxf(old, d);
+            x[k] -= m[k];
+            f[k] = ex2(old - m[k]);
             l[k] *= f[k];
           }
-          soft_sync();
-          if (quad == 0 && lane < RN)
-            mref[lane] = fmaxf(mref[lane], fmaxf(fmaxf(red[lane], red[RN + lane]), fmaxf(red[2 * RN + lane], red[3 * RN + lane])));
-          soft_sync();  // (red is free again)
+          soft_sync(half);  // (hred is free again)
           if (st > 0) {
             // the sums so far, once no product adds to them
             wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
             fence_after();
 #pragma unroll
             for (int h = 0; h < G::kHalves; ++h) {
-              float o[RN];
-              tmem_ld<RN>(tl + G::cO + h * NM, o);
+              float o[RH];
+              tmem_ld<RH>(tl + G::cO + h * NM + k0, o);
 #pragma unroll
-              for (int k = 0; k < RN; ++k) o[k] *= f[k];
-              tmem_st<RN>(tl + G::cO + h * NM, o);
+              for (int k = 0; k < RH; ++k) o[k] *= f[k];
+              tmem_st<RH>(tl + G::cO + h * NM + k0, o);
             }
           }
+          numerators();
         }
-        if (i >= 2) wait(B.pv + b, (i - 2) >> 1);  // the product has read the numerators before these
-        uint8_t* ps = sm + G::oP + b * G::kP + quad * (NM * 128) + (lane & 3) * 4;
 #pragma unroll
-        for (int k = 0; k < RN; ++k) {
-          const float p = to_tf32(ex2(x[k]));
-          l[k] += p;
-          *reinterpret_cast<float*>(ps + k * 128 + (((lane >> 2) ^ (k & 7)) << 4)) = p;
-        }
+        for (int k = 0; k < RH; ++k) l[k] += p[k];
         fence_proxy();
         fence_before();
         __syncwarp();
@@ -630,26 +683,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       }
 
       // ---- the part's sums and averages
-      const float lw = warp_sum_of<RN>(l);
-      if (lane < RN) lsum[quad * RN + lane] = lw;
+      const float lw = warp_sum_of<RH>(l);
+      if (lane < RH) hsum[quad * RH + lane] = lw;
       wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
       fence_after();
-      soft_sync();
+      soft_sync(half);
       const bool whole = s.k0 == 0 && s.k1 == s.q.n;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (s.k0 == 0 ? 1 : 0);
       float* po = a.part + slot * RN * D;
       float* pml = a.part + 2 * (int64_t)a.ctas * RN * D + slot * RN * 2;
 #pragma unroll
       for (int h = 0; h < G::kHalves; ++h) {
-        float o[RN];
-        tmem_ld<RN>(tl + G::cO + h * NM, o);
+        float o[RH];
+        tmem_ld<RH>(tl + G::cO + h * NM + k0, o);
         const int ch = 128 * h + tok;  // (D 64: the upper lanes hold zeros)
         if (tok < G::CH) {
 #pragma unroll
-          for (int k = 0; k < RN; ++k) {
+          for (int kk = 0; kk < RH; ++kk) {
+            const int k = k0 + kk;
             if (k < nrow) {
-              const float sum = (lsum[k] + lsum[RN + k]) + (lsum[2 * RN + k] + lsum[3 * RN + k]);
-              float v = sum == 0.f ? 0.f : o[k] / sum;
+              const float sum = (hsum[kk] + hsum[RH + kk]) + (hsum[2 * RH + kk] + hsum[3 * RH + kk]);
+              float v = sum == 0.f ? 0.f : o[kk] / sum;
               if (nanrow[k] >> (ch >> 5) & 1) v = __uint_as_float(0x7FC00000u);
               if (whole) {
                 const int rho = first + k, tk = rho / a.G;
@@ -657,14 +711,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
                     __bfloat16_as_ushort(__float2bfloat16_rn(v));
               } else {
                 po[k * D + ch] = v;
-                if (h == 0 && tok == 0) *reinterpret_cast<float2*>(pml + 2 * k) = make_float2(mref[k], sum);
+                if (h == 0 && tok == 0) *reinterpret_cast<float2*>(pml + 2 * k) = make_float2(m[kk], sum);
               }
             }
           }
         }
       }
       u += (uint32_t)(s.k1 - s.k0);
-      if (u >= u1 && quad == 0 && lane == 0) {
+      if (u >= u1 && warp == 4 && lane == 0) {
         JoinRec rec;
         rec.last = s.k0 == 0 && !whole ? (int)((s.item + (uint32_t)s.q.n - 1) / per) : -1;
         rec.row0 = row0, rec.first = first, rec.head = s.h, rec.rows = nrow;
@@ -672,14 +726,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         recs[blockIdx.x] = rec;
       }
       fence_before();
-      soft_sync();  // (the next part's notes overwrite these)
+      soft_sync(half);  // (the next part's notes overwrite these)
     }
   } else {
     // ----------------------------------------- cached bytes into the tensor cores' operands ----
-    const int j = warp - kLayWarp, g = lane >> 2, c = lane & 3;
-    uint32_t i = 0, seg = 0;
+    const int j = warp - kLayWarp, g = lane >> 2, c = lane & 3, t = lane & 15;
+    // where this lane's words go in a step's operands: keys, word w = 4 v + x is block w mod NB of
+    // token 8 (w / NB) + g; values, piece 8 v + g of transposed matrix cc is block (8 v + g) mod NB of
+    // token 8 (ho / 2) + 2 cc + ho mod 2, ho = (8 v + g) / NB; scales, a word of the token's row
+    uint32_t ko[NB], vo[4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) ko[b] = (16 * j + g) * 128 + ((b ^ g) << 4) + 4 * c;
+    {
+      const int ho = g / NB, b = g % NB;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const int tt = 8 * (ho >> 1) + 2 * cc + (ho & 1);
+        vo[cc] = (D == 256 ? 16384 : 0) + (16 * j + tt) * 128 + (((D == 256 ? b : 4 + b) ^ (tt & 7)) << 4) + 4 * c;
+      }
+    }
+    const uint32_t so = (lane < 16 ? 0 : 512 * G::kAtoms) + 16 * ((16 * j + t) & 31) + 4 * ((16 * j + t) >> 5);
+    const uint32_t va = ((lane & 7) * 4 + (lane >> 3)) * 16;  // of the transposing loads
+    const uint32_t vsel = (2 * (t >> 3) + (t & 1)) * 0x11u + 0x40u;  // this token's byte of two words
+    Ring<G::kRaw> raw;
+    Ring<G::kOps> op;
+    Ring<G::kQs> qr;
+    uint32_t i = 0;
     int r = r0;
-    for (uint32_t u = u0; u < u1; ++seg) {
+    for (uint32_t u = u0; u < u1; qr.next()) {
       const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
       r = s.r;
       const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first), row0 = starts[s.r];
@@ -687,39 +761,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
       // the item's queries: bf16 to tf32, rows of 32 channels
       {
-        const uint32_t qb = seg % G::kQs;
-        if (seg >= (uint32_t)G::kQs) wait(B.q_empty + qb, seg / G::kQs - 1);
-        uint8_t* dst = sm + G::oQ + qb * G::kQ;
+        uint8_t* dst = sm + G::oQ + qr.i * G::kQ;
+        constexpr int E = (D + 127) / 128, R8 = NM / 8;
+        uint2 qv[R8][E];
 #pragma unroll
-        for (int rr = 0; rr < (NM + 7) / 8; ++rr) {
-          const int k = j + 8 * rr;
-          if (k < NM) {
-            const int rho = first + k, tk = rho / a.G;
-            const uint16_t* p = a.q + (row0 + tk) * a.ldq + (int64_t)(s.h * a.G + rho - tk * a.G) * D;
+        for (int rr = 0; rr < R8; ++rr) {
+          const int k = j + 8 * rr, rho = first + k, tk = rho / a.G;
+          const uint16_t* p = a.q + (row0 + tk) * a.ldq + (int64_t)(s.h * a.G + rho - tk * a.G) * D;
 #pragma unroll
-            for (int e = 0; e < (D + 127) / 128; ++e) {
-              const int ch = 128 * e + 4 * lane;
-              if (ch < D) {
-                uint2 v = make_uint2(0, 0);
-                if (k < nrow) v = *reinterpret_cast<const uint2*>(p + ch);
-                *reinterpret_cast<uint4*>(dst + (ch >> 5) * (NM * 128) + k * 128 + ((((ch & 31) >> 2) ^ (k & 7)) << 4)) =
-                    make_uint4(v.x << 16, v.x & 0xFFFF0000u, v.y << 16, v.y & 0xFFFF0000u);
-              }
-            }
+          for (int e = 0; e < E; ++e) {
+            const int ch = 128 * e + 4 * lane;
+            qv[rr][e] = k < nrow && ch < D ? *reinterpret_cast<const uint2*>(p + ch) : make_uint2(0, 0);
           }
         }
+        wait(B.q_empty + qr.i, qr.ph ^ 1);
+#pragma unroll
+        for (int rr = 0; rr < R8; ++rr)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int k = j + 8 * rr, ch = 128 * e + 4 * lane;
+            const uint2 v = qv[rr][e];
+            if (ch < D)
+              *reinterpret_cast<uint4*>(dst + (ch >> 5) * (NM * 128) + k * 128 + ((((ch & 31) >> 2) ^ (k & 7)) << 4)) =
+                  make_uint4(v.x << 16, v.x & 0xFFFF0000u, v.y << 16, v.y & 0xFFFF0000u);
+          }
         fence_proxy();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B.q_full + qb);
+        if (lane == 0) mbar_arrive(B.q_full + qr.i);
       }
-      for (int st = 0; st < steps; ++st, ++i) {
-        const uint32_t rs = i % G::kRaw, op = i % G::kOps;
-        if (i >= (uint32_t)G::kOps) wait(B.op_empty + op, i / G::kOps - 1);
-        wait(B.raw_full + rs, i / G::kRaw);
-        const uint8_t* tp = sm + G::oRaw + rs * G::kStep + j * G::kTile;
-        uint8_t* ob = sm + G::oOp + op * G::kOp;
-        uint8_t* sb = sm + G::oSf + op * G::kSf;
-        const int t0 = raw_info[rs * 12 + j], full = raw_info[rs * 12 + 8];
+      for (int st = 0; st < steps; ++st, ++i, raw.next(), op.next()) {
+        wait(B.raw_full + raw.i, raw.ph);
+        const uint8_t* tp = sm + G::oRaw + raw.i * G::kStep + j * G::kTile;
         // keys: lane (g, c) holds 8 channels of each block of tokens g and g + 8
         uint32_t kw[D / 16], vw[D / 16];
 #pragma unroll
@@ -729,80 +801,86 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         }
         // values: a transposing load turns the pieces of lanes g = 0..7 into 4 bytes of a row each
 #pragma unroll
-        for (int v = 0; v < D / 64; ++v) {
-          const uint32_t ad = smem_u32(tp + 8 * D + v * 512 + ((lane & 7) * 4 + (lane >> 3)) * 16);
+        for (int v = 0; v < D / 64; ++v)
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                        : "=r"(vw[4 * v]), "=r"(vw[4 * v + 1]), "=r"(vw[4 * v + 2]), "=r"(vw[4 * v + 3])
-                       : "r"(ad));
-        }
-        // scales: lanes 0..15 a token's of its keys, lanes 16..31 of its values
-        const int t = lane & 15;
+                       : "r"(smem_u32(tp) + 8 * D + v * 512 + va));
+        // scales of token t: lanes 0..15 of its keys, lanes 16..31 of its values (a byte of each word)
         uint32_t sw[G::kAtoms];
-        if (lane < 16) {
-          const uint8_t* p = tp + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
-          if constexpr (NB == 2) sw[0] = *reinterpret_cast<const uint16_t*>(p);
-          else
-#pragma unroll
-            for (int at = 0; at < G::kAtoms; ++at) sw[at] = reinterpret_cast<const uint32_t*>(p)[at];
-        } else {
-          const uint8_t* p = tp + 16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + (t >> 3) * 2 + (t & 1);
+        {
+          const uint8_t* kp = tp + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
+          const uint32_t* vp = reinterpret_cast<const uint32_t*>(tp + 16 * D + D / 2 + ((t & 7) >> 1) * (D / 8));
 #pragma unroll
           for (int at = 0; at < G::kAtoms; ++at) {
-            sw[at] = 0;
-#pragma unroll
-            for (int b = 0; b < (NB < 4 ? NB : 4); ++b) sw[at] |= (uint32_t)p[16 * at + 4 * b] << (8 * b);
+            uint32_t k4, w[4] = {0, 0, 0, 0};
+            if constexpr (NB == 2) {
+              k4 = *reinterpret_cast<const uint16_t*>(kp);
+              const uint2 x = *reinterpret_cast<const uint2*>(vp);
+              w[0] = x.x, w[1] = x.y;
+            } else {
+              k4 = reinterpret_cast<const uint32_t*>(kp)[at];
+              const uint4 x = reinterpret_cast<const uint4*>(vp)[at];
+              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            }
+            uint32_t v4 = __byte_perm(w[0], w[1], vsel);
+            v4 = NB == 2 ? v4 & 0xFFFFu : __byte_perm(v4, __byte_perm(w[2], w[3], vsel), 0x5410);
+            sw[at] = lane < 16 ? k4 : v4;
           }
         }
-        const bool unseen = t0 < 0 || t0 + t > pmax;
-        uint32_t fl = 0;
+        const int t0 = raw_info[raw.i * 20 + j], full = raw_info[raw.i * 20 + 8 + j];
+        uint32_t nan = 0;
 #pragma unroll
-        for (int at = 0; at < G::kAtoms; ++at) {
-          const uint32_t nan = unseen ? 0u : ff_bytes(sw[at]);
-          fl |= nan << (4 * at);
-          // a token that no row sees, or a NaN scale (reported in the flags): zero
-          if (unseen) sw[at] = 0;
-          else if (nan) sw[at] &= ~(((nan & 1) * 0xFFu) | ((nan >> 1 & 1) * 0xFF00u) | ((nan >> 2 & 1) * 0xFF0000u) |
-                                    ((nan >> 3 & 1) * 0xFF000000u));
+        for (int at = 0; at < G::kAtoms; ++at) nan |= ((sw[at] & 0x7F7F7F7Fu) + 0x01010101u) & sw[at] & 0x80808080u;
+        Info& inf = infos[i % kInfos];
+        const bool plain = full && !__any_sync(~0u, nan != 0);
+        if (!plain) {
+          // zero scales for tokens that no row sees, and for NaN scales, which the flags report
+          const bool unseen = t0 < 0 || t0 + t > pmax;
+          uint32_t fl = 0;
+#pragma unroll
+          for (int at = 0; at < G::kAtoms; ++at) {
+            const uint32_t f = unseen ? 0u : ff_bytes(sw[at]);
+            fl |= f << (4 * at);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (unseen || (f >> b & 1)) sw[at] &= ~(0xFFu << (8 * b));
+          }
+          const uint32_t vfl = __shfl_sync(~0u, fl, 16 + t);
+          if (lane < 16) inf.flags[16 * j + t] = (uint16_t)((fl ? 0x8000u : 0u) | vfl);
+          if (lane == 16) inf.t0[j] = t0;
         }
-        const uint32_t kfl = __shfl_sync(~0u, fl, t);           // of the token's keys
-        const uint32_t vfl = __shfl_sync(~0u, fl, 16 + t);      // and values
-        // stores
+        if (lane == 16) reinterpret_cast<uint8_t*>(&inf.plain)[j] = plain;
+        wait(B.op_empty + op.i, op.ph ^ 1);
+        uint8_t* ob = sm + G::oOp + op.i * G::kOp;
 #pragma unroll
-        for (int w = 0; w < D / 16; ++w) {
-          const int hh = w / NB, b = w % NB;
-          *reinterpret_cast<uint32_t*>(ob + (16 * j + 8 * hh + g) * 128 + ((b ^ g) << 4) + 4 * c) = kw[w];
-        }
+        for (int w = 0; w < D / 16; ++w) *reinterpret_cast<uint32_t*>(ob + ko[w % NB] + (w / NB) * 1024) = kw[w];
+        // (a vector v further is 8 / NB values of ho: D 64 has one, D 128 8 tokens, D 256 one of the two
+        // tokens of a pair, whose rows differ in their swizzle)
 #pragma unroll
-        for (int v = 0; v < D / 64; ++v) {
-          const int piece = 8 * v + (lane >> 2), ho = piece / NB, b = piece % NB;
+        for (int v = 0; v < D / 64; ++v)
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
-            const int tt = 8 * (ho >> 1) + 2 * cc + (ho & 1);
-            uint8_t* row = ob + (D == 256 ? 16384 : 0) + (16 * j + tt) * 128;
-            *reinterpret_cast<uint32_t*>(row + (((D == 256 ? b : 4 + b) ^ (tt & 7)) << 4) + 4 * c) = vw[4 * v + cc];
+            uint32_t o = vo[cc];
+            if (D == 128) o += 1024 * v;
+            if (D == 256) o = ((o + 128 * (v & 1)) ^ (16u * (v & 1))) + 1024 * (v >> 1);
+            *reinterpret_cast<uint32_t*>(ob + o) = vw[4 * v + cc];
           }
-        }
-        const int mrow = 16 * j + t;
+        uint8_t* sb = sm + G::oSf + op.i * G::kSf + so;
 #pragma unroll
-        for (int at = 0; at < G::kAtoms; ++at)
-          *reinterpret_cast<uint32_t*>(sb + (lane < 16 ? 0 : 512 * G::kAtoms) + 512 * at + 16 * (mrow & 31) + 4 * (mrow >> 5)) = sw[at];
-        Info& inf = infos[i % kInfos];
-        if (lane < 16) inf.flags[mrow] = (uint16_t)((kfl ? 0x8000u : 0u) | vfl);
-        if (lane == 16) inf.t0[j] = t0;
-        if (lane == 17 && j == 0) inf.full = full;
+        for (int at = 0; at < G::kAtoms; ++at) *reinterpret_cast<uint32_t*>(sb + 512 * at) = sw[at];
         fence_proxy();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(B.raw_empty + rs);
+          mbar_arrive(B.raw_empty + raw.i);
           mbar_arrive(B.info + i % kInfos);
-          mbar_arrive(B.op_full + op);
+          mbar_arrive(B.op_full + op.i);
         }
       }
       u += (uint32_t)(s.k1 - s.k0);
     }
   }
 
-  if (dead()) {  // let the copies and products in flight end before their memory goes
+  if (*reinterpret_cast<volatile int*>(&s_dead)) {  // let the copies and products in flight end before their memory goes
     const int64_t t0 = clock64();
     while (clock64() - t0 < 2000000) __nanosleep(1000);
   }
