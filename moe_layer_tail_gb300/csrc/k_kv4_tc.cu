@@ -95,8 +95,8 @@ struct Geo {
   static constexpr int kSf = 2 * kAtoms * 512;           // key atoms, then value atoms
   static constexpr int kP = NM * 512, kQ = NM * D * 4;
   // tensor-memory columns
-  static constexpr int cK = 0, cV = 256, cS = 384, cO = cS + 2 * NM;  // (K' twice, V' once)
-  static constexpr int cSfK = cO + kHalves * NM, cSfV = cSfK + 8 * kAtoms, cSfI = cSfV + 4 * kAtoms, cSfJ = cSfI + 4;
+  static constexpr int cK = 0, cV = 128, cS = 384, cO = cS + 2 * NM;  // (K' once, V' twice)
+  static constexpr int cSfK = cO + kHalves * NM, cSfV = cSfK + 8 * kAtoms, cSfI = cSfV + 8 * kAtoms, cSfJ = cSfI + 4;
   static_assert(cSfJ + 4 <= 512, "tensor memory");
   // shared memory (from a 1024-byte boundary)
   static constexpr int oOp = 0, oI = oOp + kOps * kOp, oQ = oI + 16384, oP = oQ + kQs * kQ;
@@ -310,12 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   B.q_full = B.info + kInfos;
   B.q_empty = B.q_full + 2;
   B.k_full = B.q_empty + 2;
-  B.s_full = B.k_full + 4;
-  B.k_free = G::kHalves > 1 ? B.k_full + 2 : B.s_full;  // (one half: the scores are all that use them)
+  B.k_free = B.k_full + 1;  // (two halves only: with one, the scores are all that use the keys)
+  B.s_full = B.k_free + 1;
   B.p_full = B.s_full + 2;
   B.v_full = B.p_full + 2;
-  B.v_free = B.v_full + 1;
-  B.pv = B.v_free + 1;
+  B.v_free = B.v_full + 2;  // (two halves only)
+  B.pv = B.v_free + 2;
   B.soft = B.pv + 2;
   int* raw_info = reinterpret_cast<int*>(bp + G::kBars);  // [kRaw][20]: t0 of the tiles, full
   float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 20);  // [4][RN]
@@ -381,6 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       if (gone) return;
     }
   };
+  // both, asked for together
+  auto wait2 = [&](uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1) {
+    const bool d0 = mbar_test(b0, p0 & 1), d1 = mbar_test(b1, p1 & 1);
+    if (!d0) wait(b0, p0);
+    if (!d1) wait(b1, p1);
+    __syncwarp();
+  };
   const int r0 = u0 < u1 ? find_req(pre, a.reqs, u0) : 0;
 
   if (warp == 0) {
@@ -432,19 +439,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     // The warp stays together; each run of products is one elected thread's (the same every time),
     // whose operands the compiler then keeps in uniform registers: 9 cycles an instruction instead
     // of 46 from a divergent thread.  Sub-step n is half n % kHalves (of the channels) of step n /
-    // kHalves; the dequantised keys of the next one are asked for before the scores of this one,
-    // where its operands are there.
+    // kHalves.
     const uint32_t base = smem_u32(sm);
     const uint64_t dI = sw128_desc(base + G::oI);
     if (elect_one()) cp_sf(tm + G::cSfI, sf_desc(base + G::oSfI));
     __syncwarp();
-    Ring<G::kOps> ahead;  // the operands of the next sub-step whose keys are asked for
+    Ring<G::kOps> op;  // of the keys asked for next
     auto k_ident = [&](uint32_t n) {
-      const uint32_t h = n % G::kHalves, nb = n & 1;
-      const uint32_t ob = base + G::oOp + ahead.i * G::kOp, sb = base + G::oSf + ahead.i * G::kSf;
+      const uint32_t h = n % G::kHalves;
+      const uint32_t ob = base + G::oOp + op.i * G::kOp, sb = base + G::oSf + op.i * G::kSf;
       const uint32_t sf = tm + G::cSfK + (n / G::kHalves & 1) * 4 * G::kAtoms;
-      if (h == 0) wait(B.op_full + ahead.i, ahead.ph);
-      wait(B.k_free + nb, (n >> 1) + 1);  // the scores two sub-steps ago
+      if (h == 0) wait(B.op_full + op.i, op.ph);
+      if (n > 0) {  // the scores of the sub-step before: the keys are used up
+        if (G::kHalves > 1) wait(B.k_free, n - 1);
+        else wait(B.s_full + ((n - 1) & 1), (n - 1) >> 1);
+      }
       fence_after();
       if (elect_one()) {
         if (h == 0) {
@@ -452,16 +461,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           for (int at = 0; at < G::kAtoms; ++at) cp_sf(sf + 4 * at, sf_desc(sb + 512 * at));
         }
         const uint64_t dK = sw128_desc(ob + 64 * h);
-        const uint32_t d = tm + G::cK + 128 * nb;
 #pragma unroll
         for (int k = 0; k < G::CH / 64; ++k)
-          mma_mxf4(d, dK + (uint64_t)(2 * k), dI + (uint64_t)(2 * k), idesc_mxf4(G::CH, 2 * k), sf + 4 * h,
+          mma_mxf4(tm + G::cK, dK + (uint64_t)(2 * k), dI + (uint64_t)(2 * k), idesc_mxf4(G::CH, 2 * k), sf + 4 * h,
                    tm + G::cSfI, k > 0);
-        commit(B.k_full + nb);
-        if (h + 1 == G::kHalves) commit(B.op_empty + ahead.i);
+        commit(B.k_full);
+        if (h + 1 == G::kHalves) commit(B.op_empty + op.i);
       }
       __syncwarp();
-      if (h + 1 == G::kHalves) ahead.next();
+      if (h + 1 == G::kHalves) op.next();
     };
     uint32_t n = 0;
     Ring<G::kQs> qr;
@@ -476,28 +484,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       wait(B.q_full + qr.i, qr.ph);
       for (int st = 0; st < subs; ++st, ++n) {
         if (__any_sync(~0u, gone)) break;
-        const uint32_t i = n / G::kHalves, h = n % G::kHalves, nb = n & 1, ib = i & 1;
-        bool next = st + 1 < subs || u < u1;
-        if (next && (h + 1 < G::kHalves || __all_sync(~0u, mbar_test(B.op_full + ahead.i, ahead.ph)))) {
-          k_ident(n + 1);
-          next = false;
-        }
-        if (h == 0) wait(B.p_full + ib, (i >> 1) + 1);  // the scores two steps ago are read
-        wait(B.k_full + nb, n >> 1);
+        const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1;
+        // the keys are there, the scores two steps ago are read
+        wait2(B.k_full, n, B.p_full + ib, (i >> 1) + 1);
         fence_after();
         if (elect_one()) {
           const uint64_t dQ = sw128_desc(q0 + h * (NM * 512));
-          const uint32_t d = tm + G::cS + ib * NM, ak = tm + G::cK + 128 * nb;
+          const uint32_t d = tm + G::cS + ib * NM;
 #pragma unroll
           for (int k = 0; k < G::CH / 8; ++k)
-            mma_tf32(d, ak + 8 * k, dQ + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM),
-                     k > 0 ? 1u : h);
-          if (G::kHalves > 1) commit(B.k_free + nb);
+            mma_tf32(d, tm + G::cK + 8 * k, dQ + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4),
+                     idesc_tf32(NM), k > 0 ? 1u : h);
+          if (G::kHalves > 1) commit(B.k_free);
           if (h + 1 == G::kHalves) commit(B.s_full + ib);
           if (st + 1 == subs) commit(B.q_empty + qr.i);
         }
         __syncwarp();
-        if (next) k_ident(n + 1);
+        if (st + 1 < subs || u < u1) k_ident(n + 1);
       }
       if (__any_sync(~0u, gone)) break;
     }
@@ -507,9 +510,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     const uint64_t dI = sw128_desc(base + G::oI);
     if (elect_one()) cp_sf(tm + G::cSfJ, sf_desc(base + G::oSfI));
     __syncwarp();
+    Ring<G::kOps> op;  // of the values asked for next
+    auto v_ident = [&](uint32_t n) {
+      const uint32_t h = n % G::kHalves, nb = n & 1;
+      const uint32_t ob = base + G::oOp + op.i * G::kOp, sb = base + G::oSf + op.i * G::kSf + 512 * G::kAtoms;
+      const uint32_t sf = tm + G::cSfV + (n / G::kHalves & 1) * 4 * G::kAtoms;
+      // the operands, and the product two sub-steps ago that read the values in this place
+      wait2(B.op_full + op.i, op.ph, (G::kHalves > 1 ? B.v_free : B.pv) + nb, (n >> 1) + 1);
+      fence_after();
+      if (elect_one()) {
+        if (h == 0) {
+#pragma unroll
+          for (int at = 0; at < G::kAtoms; ++at) cp_sf(sf + 4 * at, sf_desc(sb + 512 * at));
+        }
+        const uint64_t dV = sw128_desc(ob + (D == 256 ? 16384 + 64 * h : 64));
+        const uint32_t d = tm + G::cV + 128 * nb;
+#pragma unroll
+        for (int k = 0; k < G::CH / 64; ++k)
+          mma_mxf4(d, dI + (uint64_t)(2 * k), dV + (uint64_t)(2 * k), idesc_mxf4(128, 2 * k), tm + G::cSfJ,
+                   sf + 4 * h, k > 0);
+        commit(B.v_full + nb);
+        if (h + 1 == G::kHalves) commit(B.op_empty + op.i);
+      }
+      __syncwarp();
+      if (h + 1 == G::kHalves) op.next();
+    };
     uint32_t n = 0;
-    Ring<G::kOps> op;
     int r = r0;
+    if (u0 < u1) v_ident(0);
     for (uint32_t u = u0; u < u1;) {
       const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
       r = s.r;
@@ -517,42 +545,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       const int subs = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles * G::kHalves;
       for (int st = 0; st < subs; ++st, ++n) {
         if (__any_sync(~0u, gone)) break;
-        const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1;
-        const uint32_t ob = base + G::oOp + op.i * G::kOp, sb = base + G::oSf + op.i * G::kSf + 512 * G::kAtoms;
-        if (h == 0) wait(B.op_full + op.i, op.ph);
-        // the product that read the values before these
-        if (G::kHalves > 1) wait(B.v_free, n + 1);
-        else wait(B.pv + (ib ^ 1), ((n + 1) >> 1) + 1);
-        fence_after();
-        if (elect_one()) {
-          if (h == 0) {
-#pragma unroll
-            for (int at = 0; at < G::kAtoms; ++at) cp_sf(tm + G::cSfV + 4 * at, sf_desc(sb + 512 * at));
-          }
-          const uint64_t dV = sw128_desc(ob + (D == 256 ? 16384 + 64 * h : 64));
-#pragma unroll
-          for (int k = 0; k < G::CH / 64; ++k)
-            mma_mxf4(tm + G::cV, dI + (uint64_t)(2 * k), dV + (uint64_t)(2 * k), idesc_mxf4(128, 2 * k),
-                     tm + G::cSfJ, tm + G::cSfV + 4 * h, k > 0);
-          commit(B.v_full);
-          if (h + 1 == G::kHalves) commit(B.op_empty + op.i);
+        const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1, nb = n & 1;
+        bool next = st + 1 < subs || u < u1;
+        if (next && __all_sync(~0u, mbar_test(B.op_full + op.i, op.ph))) {
+          v_ident(n + 1);
+          next = false;
         }
-        __syncwarp();
-        if (h + 1 == G::kHalves) op.next();
-        if (h == 0) wait(B.p_full + ib, i >> 1);
-        wait(B.v_full, n);
+        wait2(B.v_full + nb, n >> 1, B.p_full + ib, i >> 1);
         fence_after();
         if (elect_one()) {
           const uint64_t dP = sw128_desc(base + G::oP + ib * G::kP);
-          const uint32_t d = tm + G::cO + h * NM, keep = st < G::kHalves ? 0u : 1u;
+          const uint32_t d = tm + G::cO + h * NM, av = tm + G::cV + 128 * nb, keep = st < G::kHalves ? 0u : 1u;
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            mma_tf32(d, tm + G::cV + 8 * k, dP + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4),
-                     idesc_tf32(NM), k > 0 ? 1u : keep);
-          if (G::kHalves > 1) commit(B.v_free);
+            mma_tf32(d, av + 8 * k, dP + (uint64_t)(((k >> 2) * NM * 128 + (k & 3) * 32) >> 4), idesc_tf32(NM),
+                     k > 0 ? 1u : keep);
+          if (G::kHalves > 1) commit(B.v_free + nb);
           if (h + 1 == G::kHalves) commit(B.pv + ib);
         }
         __syncwarp();
+        if (next) v_ident(n + 1);
       }
       if (__any_sync(~0u, gone)) break;
     }
@@ -592,10 +604,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         const Info& inf = infos[i % kInfos];
         const uint32_t sa = tl + G::cS + b * NM + k0;
         wait(B.s_full + b, i >> 1);
-        wait(B.info + i % kInfos, i / kInfos);
         fence_after();
+        // the notes of the step, and the product that read the numerators before these (both are
+        // there by now as a rule: their tests run beside the load)
+        const bool d0 = mbar_test(B.info + i % kInfos, i / kInfos & 1), d1 = mbar_test(B.pv + b, ((i >> 1) + 1) & 1);
         float x[RH];
         tmem_ld<RH>(sa, x);
+        if (!d0) wait(B.info + i % kInfos, i / kInfos);
         uint32_t seen = ~0u, fl = 0;
         if (inf.plain != 0x0101010101010101ull) {
           int t0 = inf.t0[tok >> 4], t = t0 < 0 ? INT32_MAX : t0 + (tok & 15);
@@ -622,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           over[4 * b + quad] = mine;
           mbar_arrive(B.soft + 2 * half + b);
         }
-        wait(B.pv + b, (i >> 1) + 1);  // the product has read the numerators before these
+        if (!d1) wait(B.pv + b, (i >> 1) + 1);
         const uint32_t pb = b * G::kP;
         float p[RH];
         auto numerators = [&]() {
@@ -732,21 +747,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     // ----------------------------------------- cached bytes into the tensor cores' operands ----
     const int j = warp - kLayWarp, g = lane >> 2, c = lane & 3, t = lane & 15;
     // where this lane's words go in a step's operands: keys, word w = 4 v + x is block w mod NB of
-    // token 8 (w / NB) + g; values, piece 8 v + g of transposed matrix cc is block (8 v + g) mod NB of
-    // token 8 (ho / 2) + 2 cc + ho mod 2, ho = (8 v + g) / NB; scales, a word of the token's row
-    uint32_t ko[NB], vo[4];
+    // token 8 (w / NB) + g; values, the four words of a transposing load are block (8 v + g) mod NB of
+    // token 8 (ho / 2) + 2 c + ho mod 2, ho = (8 v + g) / NB; scales, a word of the token's row
+    uint32_t ko[NB], vo;
 #pragma unroll
     for (int b = 0; b < NB; ++b) ko[b] = (16 * j + g) * 128 + ((b ^ g) << 4) + 4 * c;
     {
       const int ho = g / NB, b = g % NB;
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        const int tt = 8 * (ho >> 1) + 2 * cc + (ho & 1);
-        vo[cc] = (D == 256 ? 16384 : 0) + (16 * j + tt) * 128 + (((D == 256 ? b : 4 + b) ^ (tt & 7)) << 4) + 4 * c;
-      }
+      const int tt = 8 * (ho >> 1) + 2 * c + (ho & 1);
+      vo = (D == 256 ? 16384 : 0) + (16 * j + tt) * 128 + (((D == 256 ? b : 4 + b) ^ (tt & 7)) << 4);
     }
     const uint32_t so = (lane < 16 ? 0 : 512 * G::kAtoms) + 16 * ((16 * j + t) & 31) + 4 * ((16 * j + t) >> 5);
-    const uint32_t va = ((lane & 7) * 4 + (lane >> 3)) * 16;  // of the transposing loads
+    // of the transposing loads: matrix x takes rows (c, g) for g = 2 x, 2 x + 1, 128 bytes side by side
+    const uint32_t va = ((2 * (lane >> 3) + (lane & 1)) * 4 + ((lane & 7) >> 1)) * 16;
     const uint32_t vsel = (2 * (t >> 3) + (t & 1)) * 0x11u + 0x40u;  // this token's byte of two words
     Ring<G::kRaw> raw;
     Ring<G::kOps> op;
@@ -799,7 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           const uint4 x = *reinterpret_cast<const uint4*>(tp + v * 512 + lane * 16);
           kw[4 * v] = x.x, kw[4 * v + 1] = x.y, kw[4 * v + 2] = x.z, kw[4 * v + 3] = x.w;
         }
-        // values: a transposing load turns the pieces of lanes g = 0..7 into 4 bytes of a row each
+        // values: a transposing load brings the pieces of lanes g = 0..7 (4 bytes from each two) of one
+        // token and block together: 16 bytes of its row
 #pragma unroll
         for (int v = 0; v < D / 64; ++v)
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -857,14 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         // (a vector v further is 8 / NB values of ho: D 64 has one, D 128 8 tokens, D 256 one of the two
         // tokens of a pair, whose rows differ in their swizzle)
 #pragma unroll
-        for (int v = 0; v < D / 64; ++v)
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t o = vo[cc];
-            if (D == 128) o += 1024 * v;
-            if (D == 256) o = ((o + 128 * (v & 1)) ^ (16u * (v & 1))) + 1024 * (v >> 1);
-            *reinterpret_cast<uint32_t*>(ob + o) = vw[4 * v + cc];
-          }
+        for (int v = 0; v < D / 64; ++v) {
+          uint32_t o = vo;
+          if (D == 128) o += 1024 * v;
+          if (D == 256) o = ((o + 128 * (v & 1)) ^ (16u * (v & 1))) + 1024 * (v >> 1);
+          *reinterpret_cast<uint4*>(ob + o) = make_uint4(vw[4 * v], vw[4 * v + 1], vw[4 * v + 2], vw[4 * v + 3]);
+        }
         uint8_t* sb = sm + G::oSf + op.i * G::kSf + so;
 #pragma unroll
         for (int at = 0; at < G::kAtoms; ++at) *reinterpret_cast<uint32_t*>(sb + 512 * at) = sw[at];
