@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
 
   bool gone = false;  // a wait gave up, here or elsewhere in the CTA
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (mbar_sleep_wait(b, parity & 1)) return;
+    if (mbar_test(b, parity & 1)) return;  // (quicker than the waiting form where it has completed)
     const int64_t t0 = clock64();
     while (!mbar_sleep_wait(b, parity & 1)) {
       gone = *reinterpret_cast<volatile int*>(&s_dead) != 0;
