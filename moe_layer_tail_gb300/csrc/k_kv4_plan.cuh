@@ -40,42 +40,41 @@ __device__ __forceinline__ Req req_of(const AttnArgs& a, int rn, int L, int rs, 
 }
 
 // Sums the work of all requests: pre[r] = tiles before request r (shared), the lengths and row
-// starts beside it.  Returns all tiles (the same in every one of the CTA's 32 W threads).
-template <int W>
-__device__ __forceinline__ uint64_t plan(const AttnArgs& a, int rn, uint32_t* pre, int* lens,
-                                         int* starts, uint64_t* wsum, int* bits) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// starts beside it.  One warp does it, 32 requests at a time; `first` are the lengths and starts of
+// the first 32, loaded ahead.  The caller synchronises before the results are read.
+struct PlanLoad {
+  int L, rs, re;
+};
+__device__ __forceinline__ PlanLoad plan_load(const AttnArgs& a, int r) {
+  PlanLoad p = {0, 0, 0};
+  if (r < a.reqs) p.L = a.kv_lens[r], p.rs = a.row_starts[r], p.re = a.row_starts[r + 1];
+  return p;
+}
+__device__ __forceinline__ uint64_t plan(const AttnArgs& a, int rn, PlanLoad next, uint32_t* pre, int* lens,
+                                         int* starts, int* bits) {
+  const int lane = threadIdx.x & 31;
   uint64_t base = 0;
-  for (int r0 = 0; r0 < a.reqs; r0 += 32 * W) {
-    const int r = r0 + tid;
+  for (int r0 = 0; r0 < a.reqs; r0 += 32) {
+    const int r = r0 + lane;
+    const PlanLoad p = next;
+    next = plan_load(a, r + 32);
     uint64_t v = 0;
     if (r < a.reqs) {
-      const int L = a.kv_lens[r], rs = a.row_starts[r], re = a.row_starts[r + 1];
-      const Req q = req_of(a, rn, L, rs, re, bits);
+      const Req q = req_of(a, rn, p.L, p.rs, p.re, bits);
       v = (uint64_t)q.rt * (uint32_t)a.heads * (uint32_t)q.n;
-      lens[r] = L;
-      starts[r] = rs;
-      if (r == a.reqs - 1) starts[a.reqs] = re;
+      lens[r] = p.L;
+      starts[r] = p.rs;
+      if (r == a.reqs - 1) starts[a.reqs] = p.re;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t w = __shfl_up_sync(~0u, v, o);
       if (lane >= o) v += w;
     }
-    if (lane == 31) wsum[warp] = v;
-    __syncthreads();
-    uint64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) v += wsum[w];
-      all += wsum[w];
-    }
     if (r < a.reqs) pre[r + 1] = (uint32_t)(base + v);
-    base += all;
-    __syncthreads();
+    base += __shfl_sync(~0u, v, 31);
   }
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
+  if (lane == 0) pre[0] = 0;
   return base;
 }
 __device__ __forceinline__ uint32_t range_tiles(uint64_t total, int ctas) {

@@ -1,5 +1,7 @@
 // k_kv4_rows.cu -- the row-wise kernels of the decode step's attention block (kv4_attn.h):
-// step tables, query/key norm with rotation, cache rows in and out.
+// step tables, query/key norm with rotation, cache rows in and out.  Each launch is a programmatic
+// dependent launch of the kernel before it: its CTAs line up while that one ends and touch no
+// memory until it has completed.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -50,6 +52,8 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
   const int R = a.reqs;
   const bool first = blockIdx.x == 0;
   int bits = 0;
+  mtail::pdl_trigger();
+  mtail::pdl_wait();
 
   int c = 0, n = 0, have = 0, want = 0;
   bool ok = true;
@@ -149,6 +153,8 @@ __global__ void __launch_bounds__(256) k_qk_norm_rope(const RopeArgs a, int chun
   const int h0 = chunk * per * kHeads, h1 = min(heads, h0 + per * kHeads);
   const bool act = li < a.D / 8;
   const int half = a.rot / 2;
+  mtail::pdl_trigger();
+  mtail::pdl_wait();
 
   auto src = [&](int h) -> const uint4* {
     return reinterpret_cast<const uint4*>(h < a.hq ? a.q + t * a.ldq + (int64_t)h * a.D
@@ -243,6 +249,8 @@ __global__ void __launch_bounds__(256) k_kv4_append(const RowsArgs a) {
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
   const bool in = id < (int64_t)a.rows * a.heads;
   const int row = in ? (int)(id / a.heads) : 0, h = in ? (int)(id % a.heads) : 0;
+  mtail::pdl_trigger();
+  mtail::pdl_wait();
   int64_t slot = in ? a.slots[row] : -1;
   if (slot >= a.n_slots) {
     if (h == 0 && i == 0 && !val) report(a.status, kStatusBadSlot);
@@ -318,6 +326,8 @@ __global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
   const bool val = blockIdx.y != 0;
   const int64_t id = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
+  mtail::pdl_trigger();
+  mtail::pdl_wait();
   if (id >= (int64_t)a.rows * a.heads) return;
   const int row = (int)(id / a.heads), h = (int)(id % a.heads);
   const int64_t slot = a.slots[row];
@@ -359,8 +369,7 @@ cudaError_t launch_step_tables(const TablesArgs& a, cudaStream_t st) {
   // four rows a thread, at most two CTAs' worth of threads on every SM
   const int64_t want = ((int64_t)a.max_rows + 4 * threads - 1) / (4 * threads);
   const int grid = (int)std::min<int64_t>(want, 2 * num_sms());
-  k_step_tables<<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  return mtail::launch_k(k_step_tables, dim3(grid), dim3(threads), 0, st, true, a);
 }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
@@ -371,10 +380,8 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
   const int chunks = (groups + per - 1) / per;
   const int64_t grid = (int64_t)a.rows * chunks;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (L == 8) k_qk_norm_rope<8><<<(unsigned)grid, 256, 0, st>>>(a, chunks, per);
-  else if (L == 16) k_qk_norm_rope<16><<<(unsigned)grid, 256, 0, st>>>(a, chunks, per);
-  else k_qk_norm_rope<32><<<(unsigned)grid, 256, 0, st>>>(a, chunks, per);
-  return cudaGetLastError();
+  auto* kernel = L == 8 ? k_qk_norm_rope<8> : L == 16 ? k_qk_norm_rope<16> : k_qk_norm_rope<32>;
+  return mtail::launch_k(kernel, dim3((unsigned)grid), dim3(256), 0, st, true, a, chunks, per);
 }
 
 namespace {
@@ -383,13 +390,10 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
   const int per = 256 / (a.D / 8);
   const int64_t n = ((int64_t)a.rows * a.heads + per - 1) / per;  // <= 2^24 * 256 / 8
   const dim3 grid((unsigned)n, 2);
-  switch (a.D) {
-    case 64: kAppend ? k_kv4_append<64><<<grid, 256, 0, st>>>(a) : k_kv4_read<64><<<grid, 256, 0, st>>>(a); break;
-    case 128: kAppend ? k_kv4_append<128><<<grid, 256, 0, st>>>(a) : k_kv4_read<128><<<grid, 256, 0, st>>>(a); break;
-    case 256: kAppend ? k_kv4_append<256><<<grid, 256, 0, st>>>(a) : k_kv4_read<256><<<grid, 256, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  auto* kernel = a.D == 64    ? (kAppend ? k_kv4_append<64> : k_kv4_read<64>)
+                 : a.D == 128 ? (kAppend ? k_kv4_append<128> : k_kv4_read<128>)
+                              : (kAppend ? k_kv4_append<256> : k_kv4_read<256>);
+  return mtail::launch_k(kernel, grid, dim3(256), 0, st, true, a);
 }
 }  // namespace
 

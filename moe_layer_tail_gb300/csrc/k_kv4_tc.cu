@@ -105,7 +105,7 @@ struct Geo {
   static constexpr int oSmall = oInfo + kInfos * (int)sizeof(Info);
   // raw and operand rings, info ring, q, and the single ones
   static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 12 + 4;
-  static constexpr int kSmall = kBars * 8 + kRaw * 20 * 4 /* t0, full */ + 4 * RN * 8 /* red, l */ +
+  static constexpr int kSmall = kBars * 8 + kRaw * 20 * 4 /* t0, full */ + 4 * RN * 12 /* red, l */ +
                                 RN * 8 /* rowpos, nan */ + 64 + 32 /* over */;
   static constexpr size_t smem(int reqs) {
     return 1024 + (size_t)oSmall + kSmall + (size_t)(3 * reqs + 2) * 4;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   using G = Geo<D, RN>;
   constexpr int NM = G::NM, NB = G::NB;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ uint64_t wsum[kWarps];
+  __shared__ uint64_t s_total;
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead;
   uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   B.pv = B.v_free + 2;
   B.soft = B.pv + 2;
   int* raw_info = reinterpret_cast<int*>(bp + G::kBars);  // [kRaw][20]: t0 of the tiles, full
-  float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 20);  // [4][RN]
-  float* lsum = red + 4 * RN;                                       // [4][RN]
+  float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 20);  // [2][4][RN]
+  float* lsum = red + 8 * RN;                                       // [4][RN]
   int* rowpos = reinterpret_cast<int*>(lsum + 4 * RN);
   uint32_t* nanrow = reinterpret_cast<uint32_t*>(rowpos + RN);
   uint32_t* pre = nanrow + RN + 16;
@@ -329,11 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
   JoinRec* recs = reinterpret_cast<JoinRec*>(a.part + 2 * (int64_t)a.ctas * RN * (D + 2));
 
-  // ---- set-up that depends on nothing, then the plan
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
+  // ---- set-up that depends on nothing (it may run while the previous kernel ends), then the plan
   if (tid == 0) {
     s_dead = 0;
     for (int i = 0; i < G::kBars; ++i) {
@@ -343,26 +339,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // the identity (E2M1 code 2 is 1.0) in rows of 128 bytes, and its scales
-  for (int i = tid; i < 128 * 8; i += kThreads) {
-    const int r = i >> 3, ch = i & 7;
-    const uint32_t one = ch == r >> 5 ? 2u << (4 * (r & 7)) : 0u;
-    const int w = (r >> 3) & 3;
-    *reinterpret_cast<uint4*>(sm + G::oI + r * 128 + ((ch ^ (r & 7)) << 4)) =
-        make_uint4(w == 0 ? one : 0u, w == 1 ? one : 0u, w == 2 ? one : 0u, w == 3 ? one : 0u);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (tid < 32) *reinterpret_cast<uint4*>(sm + G::oSfI + tid * 16) = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  fence_proxy();
-
-  int bits = 0;
-  const uint64_t total64 = plan<kWarps>(a, RN, pre, lens, starts, wsum, &bits);
-  if (total64 > 0x7FFFFFFFull) bits |= kStatusBadLength;
-  if (blockIdx.x == 0 && bits && a.status) atomicOr(a.status, bits);
-  const uint32_t total = total64 > 0x7FFFFFFFull ? 0u : (uint32_t)total64, per = range_tiles(total, a.ctas);
-  const uint64_t u0w = (uint64_t)blockIdx.x * per;
+  if (warp == 2) {
+    mtail::pdl_wait();
+    int bits = 0;
+    const uint64_t total64 = plan(a, RN, plan_load(a, lane), pre, lens, starts, &bits);
+    if (total64 > 0x7FFFFFFFull) bits |= kStatusBadLength;
+    if (blockIdx.x == 0 && bits && a.status) atomicOr(a.status, bits);
+    if (lane == 0) s_total = total64 > 0x7FFFFFFFull ? 0 : total64;
+  } else {
+    // the identity (E2M1 code 2 is 1.0) in rows of 128 bytes, and its scales
+    for (int i = tid < 64 ? tid : tid - 32; i < 128 * 8; i += kThreads - 32) {
+      const int r = i >> 3, ch = i & 7;
+      const uint32_t one = ch == r >> 5 ? 2u << (4 * (r & 7)) : 0u;
+      const int w = (r >> 3) & 3;
+      *reinterpret_cast<uint4*>(sm + G::oI + r * 128 + ((ch ^ (r & 7)) << 4)) =
+          make_uint4(w == 0 ? one : 0u, w == 1 ? one : 0u, w == 2 ? one : 0u, w == 3 ? one : 0u);
+    }
+    if (warp == 3) *reinterpret_cast<uint4*>(sm + G::oSfI + lane * 16) = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    fence_proxy();
+    mtail::pdl_wait();
+  }
   fence_before();
   __syncthreads();
   fence_after();
+  const uint32_t total = (uint32_t)s_total, per = range_tiles(total, a.ctas);
+  const uint64_t u0w = (uint64_t)blockIdx.x * per;
   const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
   const uint32_t u0 = (uint32_t)min(u0w, (uint64_t)total), u1 = min(total, u0 + per);
   if (u0 == u1 && tid == 0) recs[blockIdx.x].last = -1;
@@ -581,8 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < (RH < 8 ? RH : 8); ++k)
       ps[k] = sm + G::oP + quad * (NM * 128) + (k0 + k) * 128 + (((lane >> 2) ^ ((k0 + k) & 7)) << 4) + (lane & 3) * 4;
-    float* hred = red + half * 4 * RH;
+    float* hred = red + half * 4 * RH;  // [2 turns][2 halves][4][RH]
     float* hsum = lsum + half * 4 * RH;
+    int turn = 0;
     uint32_t i = 0;
     int r = r0;
     for (uint32_t u = u0; u < u1;) {
@@ -661,19 +667,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
             y[k] = x[k];
           }
           const float w = warp_max_of<RH>(y);
-          if (lane < RH) hred[quad * RH + lane] = w;
+          float* hr = hred + (turn ^= 1) * 8 * RH;  // (the turn before may still be read)
+          if (lane < RH) hr[quad * RH + lane] = w;
           soft_sync(half);
           float f[RH];
 #pragma unroll
           for (int k = 0; k < RH; ++k) {
-            const float d = fmaxf(fmaxf(hred[k], hred[RH + k]), fmaxf(hred[2 * RH + k], hred[3 * RH + k]));
+            const float d = fmaxf(fmaxf(hr[k], hr[RH + k]), fmaxf(hr[2 * RH + k], hr[3 * RH + k]));
             const float old = m[k];
             m[k] = fmaxf(old, d);
             x[k] -= m[k];
             f[k] = ex2(old - m[k]);
             l[k] *= f[k];
           }
-          soft_sync(half);  // (hred is free again)
           if (st > 0) {
             // the sums so far, once no product adds to them
             wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
@@ -703,32 +709,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
       fence_after();
       soft_sync(half);
+      // the joining launch may line up now (from the start on, its CTAs had cost 2 us a call)
+      if (u + (uint32_t)(s.k1 - s.k0) >= u1) mtail::pdl_trigger();
       const bool whole = s.k0 == 0 && s.k1 == s.q.n;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (s.k0 == 0 ? 1 : 0);
-      float* po = a.part + slot * RN * D;
-      float* pml = a.part + 2 * (int64_t)a.ctas * RN * D + slot * RN * 2;
+      // lane k of each warp: where row k0 + k goes, 1 / sum and its NaN blocks
+      const int kl = k0 + (lane < RH ? lane : 0);
+      const float sum = (hsum[kl - k0] + hsum[RH + kl - k0]) + (hsum[2 * RH + kl - k0] + hsum[3 * RH + kl - k0]);
+      const float inv_l = sum == 0.f ? 0.f : 1.f / sum;
+      const uint32_t nan_l = nanrow[kl];
+      int64_t at_l;
+      if (whole) {
+        const int rho = first + kl, tk = rho / a.G;
+        at_l = (row0 + tk) * a.ldo + (int64_t)(s.h * a.G + rho - tk * a.G) * D;
+      } else {
+        at_l = (slot * RN + kl) * D;
+        float* pml = a.part + 2 * (int64_t)a.ctas * RN * D + slot * RN * 2;
+        float mk = m[0];
+#pragma unroll
+        for (int k = 1; k < RH; ++k) mk = lane == k ? m[k] : mk;
+        if (quad == 0 && lane < RH && kl < nrow) *reinterpret_cast<float2*>(pml + 2 * kl) = make_float2(mk, sum);
+      }
 #pragma unroll
       for (int h = 0; h < G::kHalves; ++h) {
         float o[RH];
         tmem_ld<RH>(tl + G::cO + h * NM + k0, o);
         const int ch = 128 * h + tok;  // (D 64: the upper lanes hold zeros)
-        if (tok < G::CH) {
 #pragma unroll
-          for (int kk = 0; kk < RH; ++kk) {
-            const int k = k0 + kk;
-            if (k < nrow) {
-              const float sum = (hsum[kk] + hsum[RH + kk]) + (hsum[2 * RH + kk] + hsum[3 * RH + kk]);
-              float v = sum == 0.f ? 0.f : o[kk] / sum;
-              if (nanrow[k] >> (ch >> 5) & 1) v = __uint_as_float(0x7FC00000u);
-              if (whole) {
-                const int rho = first + k, tk = rho / a.G;
-                a.out[(row0 + tk) * a.ldo + (int64_t)(s.h * a.G + rho - tk * a.G) * D + ch] =
-                    __bfloat16_as_ushort(__float2bfloat16_rn(v));
-              } else {
-                po[k * D + ch] = v;
-                if (h == 0 && tok == 0) *reinterpret_cast<float2*>(pml + 2 * k) = make_float2(m[kk], sum);
-              }
-            }
+        for (int k = 0; k < RH; ++k) {
+          const int64_t at = __shfl_sync(~0u, at_l, k);
+          float v = o[k] * __shfl_sync(~0u, inv_l, k);
+          if (__shfl_sync(~0u, nan_l, k) >> (ch >> 5) & 1) v = __uint_as_float(0x7FC00000u);
+          if (k0 + k < nrow && tok < G::CH) {
+            if (whole) a.out[at + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            else a.part[at + ch] = v;
           }
         }
       }
@@ -898,58 +912,84 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   }
   fence_before();
   __syncthreads();
-  mtail::pdl_trigger();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 
 // Joins the parts of the items that several ranges share.  CTA (x, y): the item that crosses the
 // end of range x for the first time, rows 4 y .. 4 y + 3, one per warp:
 //   out = sum_k w_k o_k / sum_k w_k,  w_k = l_k 2^(m_k - max m), in range order.
-template <int D>
-__global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ AttnArgs a, int rn) {
+// The first parts are on their way while the weights are formed.
+template <int D, int RN>
+__global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ AttnArgs a) {
+  extern __shared__ float sw[];  // [4][ctas]: weights of a warp's row
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  mtail::pdl_trigger();
   mtail::pdl_wait();
-  const JoinRec rec = reinterpret_cast<const JoinRec*>(a.part + 2 * (int64_t)a.ctas * rn * (D + 2))[blockIdx.x];
+  const JoinRec rec = reinterpret_cast<const JoinRec*>(a.part + 2 * (int64_t)a.ctas * RN * (D + 2))[blockIdx.x];
   const int i = blockIdx.y * 4 + warp;
   if (rec.last < 0 || i >= rec.rows) return;
-  const int c0 = blockIdx.x, c1 = rec.last;
+  const int c0 = blockIdx.x, n = rec.last - c0 + 1;
+  // part k's slot: the item begins in the second one of its first range, then takes the first ones
+  auto slot = [&](int k) { return 2 * (int64_t)(c0 + k) + (k == 0 ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(a.part + 2 * (int64_t)a.ctas * RN * D) + i;
   const float* po = a.part + (int64_t)i * D;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + 2 * (int64_t)a.ctas * rn * D) + i;
-  auto slot = [&](int k) { return 2 * (int64_t)k + (k == c0 ? 1 : 0); };
-  float m = kLow;
-  for (int k = c0 + lane; k <= c1; k += 32) m = fmaxf(m, ml[slot(k) * rn].x);
-  m = mtail::warp_max(m);
-  m = __shfl_sync(~0u, m, 0);
-  constexpr int E = D / 32;
-  float o[E], sum = 0.f;
+  float* w = sw + warp * a.ctas;
+  constexpr int E = D / 32, kAhead = 8;  // channels of a lane (2 or 4 side by side), parts on their way
+  constexpr int V = E == 2 ? 2 : 4, C = E / V;
+  float x[kAhead][E];
+  auto load = [&](int k, float* v) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float* p = po + slot(k) * RN * D + (c * 32 + lane) * V;
+      if constexpr (V == 2) {
+        const float2 t = *reinterpret_cast<const float2*>(p);
+        v[0] = t.x, v[1] = t.y;
+      } else {
+        const float4 t = *reinterpret_cast<const float4*>(p);
+        v[4 * c] = t.x, v[4 * c + 1] = t.y, v[4 * c + 2] = t.z, v[4 * c + 3] = t.w;
+      }
+    }
+  };
+  float2 mine = make_float2(kLow, 0.f);
+  if (lane < n) mine = ml[slot(lane) * RN];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < n) load(k, x[k]);
+  float m = mine.x, sum = 0.f;
+  for (int k = 32 + lane; k < n; k += 32) m = fmaxf(m, ml[slot(k) * RN].x);
+  m = __shfl_sync(~0u, mtail::warp_max(m), 0);
+  for (int k = lane; k < n; k += 32) {
+    const float2 v = k < 32 ? mine : ml[slot(k) * RN];
+    const float wk = v.y * ex2(v.x - m);
+    w[k] = wk;
+    sum += wk;
+  }
+  sum = __shfl_sync(~0u, mtail::warp_sum(sum), 0);
+  __syncwarp();
+  float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll 8
-  for (int k = c0; k <= c1; ++k) {
-    const float2 v = ml[slot(k) * rn];
-    const float w = v.y * ex2(v.x - m);
-    const float* p = po + slot(k) * rn * D + lane * E;
-    sum += w;
-    if constexpr (E == 2) {
-      const float2 x = *reinterpret_cast<const float2*>(p);
-      o[0] = fmaf(w, x.x, o[0]), o[1] = fmaf(w, x.y, o[1]);
-    } else {
+  for (int k0 = 0; k0 < n; k0 += kAhead) {
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + e);
-        o[e] = fmaf(w, x.x, o[e]), o[e + 1] = fmaf(w, x.y, o[e + 1]);
-        o[e + 2] = fmaf(w, x.z, o[e + 2]), o[e + 3] = fmaf(w, x.w, o[e + 3]);
+    for (int k = 0; k < kAhead; ++k) {
+      if (k0 + k < n) {
+        const float wk = w[k0 + k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(wk, x[k][e], o[e]);
+        if (k0 + k + kAhead < n) load(k0 + k + kAhead, x[k]);
       }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int rho = rec.first + i, tok = rho / a.G;
-  uint16_t* orow = a.out + (rec.row0 + tok) * a.ldo + (int64_t)(rec.head * a.G + rho - tok * a.G) * D + lane * E;
+  uint16_t* orow = a.out + (rec.row0 + tok) * a.ldo + (int64_t)(rec.head * a.G + rho - tok * a.G) * D;
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
-    reinterpret_cast<uint32_t*>(orow)[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
-  }
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(o[V * c + e] * inv, o[V * c + e + 1] * inv);
+      *reinterpret_cast<uint32_t*>(orow + (c * 32 + lane) * V + e) = *reinterpret_cast<const uint32_t*>(&v);
+    }
 }
 
 template <int D, int RN>
@@ -971,10 +1011,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   static_assert(Geo<D, RN>::smem(kMaxReqs) <= 232448 - 256, "shared memory");
   cudaError_t e = prepare<D, RN>();
   if (e != cudaSuccess) return e;
-  k_kv4_attn<D, RN><<<a.ctas, kThreads, Geo<D, RN>::smem(a.reqs), st>>>(a);
-  e = cudaGetLastError();
+  e = mtail::launch_k(k_kv4_attn<D, RN>, dim3(a.ctas), dim3(kThreads), Geo<D, RN>::smem(a.reqs), st, true, a);
   if (e != cudaSuccess || a.ctas < 2) return e;
-  return mtail::launch_k(k_kv4_join<D>, dim3(a.ctas - 1, RN / 4), dim3(128), 0, st, true, a, RN);
+  return mtail::launch_k(k_kv4_join<D, RN>, dim3(a.ctas - 1, RN / 4), dim3(128), (size_t)a.ctas * 4 * sizeof(float), st, true, a);
 }
 
 template <typename F>
