@@ -56,7 +56,8 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st);
 
 struct RowsArgs {
   int rows, heads, D, page;
-  int64_t n_slots;  // n_pages * page
+  int64_t n_slots;      // n_pages * page
+  uint64_t page_magic;  // ceil(2^64 / page): slot / page by a multiply
   uint8_t* cache;
   uint16_t* k;  // read by the append, written by the read
   uint16_t* v;

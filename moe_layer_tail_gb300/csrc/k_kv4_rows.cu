@@ -31,6 +31,10 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
 int num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -43,311 +47,333 @@ int num_sms() {
 //
 // Two exclusive sums over the requests (rows, pages), then every row and every fresh table
 // entry finds its request by bisection.  Each CTA sums the (at most 1024) lengths for itself:
-// 8 KB from L2, so that the launch needs no second pass.
+// 8 KB from L2, so that the launch needs no second pass.  The sums saturate at INT_MAX, which is
+// associative and above anything that is asked of them (max_rows, the entries of all tables).
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, (uint32_t)INT32_MAX); }
+
+// the last of n ascending starts (the first is 0) that is at most i
+__device__ __forceinline__ int find_start(const int* start, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (start[m] <= i) lo = m; else hi = m - 1;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
-  __shared__ int s_row[kMaxReqs + 1];    // first row of each request, cut to max_rows
-  __shared__ int s_page[kMaxReqs + 1];   // its first free page, cut to INT_MAX
-  __shared__ int64_t s_wr[32], s_wp[32];
+  __shared__ int s_row[kMaxReqs + 1];   // first row of each request, cut to max_rows
+  __shared__ int s_page[kMaxReqs + 1];  // its first fresh page
+  __shared__ int s_len[kMaxReqs], s_held[kMaxReqs];  // its cached tokens, the pages that hold them
+  __shared__ uint32_t s_wr[32], s_wp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int R = a.reqs;
-  const bool first = blockIdx.x == 0;
   int bits = 0;
   mtail::pdl_trigger();
   mtail::pdl_wait();
 
   int c = 0, n = 0, have = 0, want = 0;
-  bool ok = true;
   if (tid < R) {
     c = a.cached[tid];
     n = a.fresh[tid];
     const int64_t len = (int64_t)c + n;
-    ok = c >= 0 && n >= 0 && len <= INT32_MAX && len <= (int64_t)a.width * a.page;
-    if (!ok) bits |= kStatusBadLength, c = n = 0;
+    if (!(c >= 0 && n >= 0 && len <= INT32_MAX && len <= (int64_t)a.width * a.page))
+      bits |= kStatusBadLength, c = n = 0;
     have = c / a.page + (c % a.page != 0);
     want = n ? (c + n - 1) / a.page + 1 : have;  // (c + n <= INT_MAX)
+    s_len[tid] = c, s_held[tid] = have;
   }
-  int64_t r = n, p = want - have;
+  uint32_t r = n, p = want - have;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t r1 = __shfl_up_sync(~0u, r, o), p1 = __shfl_up_sync(~0u, p, o);
-    if (lane >= o) r += r1, p += p1;
+    const uint32_t r1 = __shfl_up_sync(~0u, r, o), p1 = __shfl_up_sync(~0u, p, o);
+    if (lane >= o) r = add_sat(r, r1), p = add_sat(p, p1);
   }
   if (lane == 31) s_wr[warp] = r, s_wp[warp] = p;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) r += s_wr[w], p += s_wp[w];
+  uint32_t wr = lane < nw ? s_wr[lane] : 0, wp = lane < nw ? s_wp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t r1 = __shfl_up_sync(~0u, wr, o), p1 = __shfl_up_sync(~0u, wp, o);
+    if (lane >= o) wr = add_sat(wr, r1), wp = add_sat(wp, p1);
+  }
+  const uint32_t all_rows = __shfl_sync(~0u, wr, 31), all_pages = __shfl_sync(~0u, wp, 31);
+  const uint32_t r0 = __shfl_sync(~0u, wr, max(warp - 1, 0)), p0 = __shfl_sync(~0u, wp, max(warp - 1, 0));
+  if (warp) r = add_sat(r, r0), p = add_sat(p, p0);
   if (tid < R) {
-    s_row[tid + 1] = (int)min(r, (int64_t)a.max_rows);
-    s_page[tid + 1] = (int)min(p, (int64_t)INT32_MAX);
+    s_row[tid + 1] = min((int)r, a.max_rows);
+    s_page[tid + 1] = (int)p;
   }
   if (tid == 0) s_row[0] = s_page[0] = 0;
-  int64_t all_rows = 0, all_pages = 0;
-  for (int w = 0; w < nw; ++w) all_rows += s_wr[w], all_pages += s_wp[w];
   __syncthreads();
 
-  if (first) {
+  if (blockIdx.x == 0) {
     if (tid < R) {
       a.row_starts[tid + 1] = s_row[tid + 1];
       a.kv_lens[tid] = c + n;
     }
     if (tid == 0) {
       a.row_starts[0] = 0;
-      a.used[0] = (int)min(all_pages, (int64_t)a.n_free);
-      if (all_pages > a.n_free) bits |= kStatusNoPages;
-      if (all_rows > a.max_rows) bits |= kStatusRows;
+      a.used[0] = min((int)all_pages, a.n_free);
+      if ((int)all_pages > a.n_free) bits |= kStatusNoPages;
+      if ((int)all_rows > a.max_rows) bits |= kStatusRows;
     }
     report(a.status, bits);
   }
 
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  const int64_t at = (int64_t)blockIdx.x * blockDim.x + tid;
+  const int step = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + tid;  // (max_rows is at most 2^20)
   const int T = s_row[R];
-  for (int64_t i = at; i < a.max_rows; i += step) {
+  for (int i = at; i < a.max_rows; i += step) {
     int pos = 0;
     int64_t slot = -1;
     if (i < T) {
-      int lo = 0, hi = R - 1;  // the last request that starts at or before row i
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (s_row[m] <= i) lo = m; else hi = m - 1;
-      }
-      const int cl = a.cached[lo];  // (valid: the request has rows)
-      pos = cl + (int)(i - s_row[lo]);
-      const int e = pos / a.page, held = cl / a.page + (cl % a.page != 0);
+      const int q = find_start(s_row, R, i);
+      pos = s_len[q] + (i - s_row[q]);
+      const int e = pos / a.page, f = e - s_held[q];
       int page;
-      if (e < held) {
-        page = a.table[lo * a.stride + e];
+      if (f < 0) {
+        page = a.table[q * a.stride + e];
       } else {
-        const int64_t f = (int64_t)s_page[lo] + (e - held);
-        page = f < a.n_free ? a.free_pages[f] : -1;
+        const int64_t g = (int64_t)s_page[q] + f;
+        page = g < a.n_free ? a.free_pages[g] : -1;
       }
-      if (page >= 0) slot = (int64_t)page * a.page + pos % a.page;
+      if (page >= 0) slot = (int64_t)page * a.page + (pos - e * a.page);
     }
     a.positions[i] = pos;
     a.slots[i] = slot;
   }
-  const int64_t P = min(all_pages, (int64_t)INT32_MAX);
-  for (int64_t i = at; i < P; i += step) {
-    int lo = 0, hi = R - 1;
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (s_page[m] <= i) lo = m; else hi = m - 1;
-    }
-    const int cl = a.cached[lo], held = cl / a.page + (cl % a.page != 0);
-    a.table[lo * a.stride + held + (i - s_page[lo])] = i < a.n_free ? a.free_pages[i] : -1;
+  for (int64_t i = at; i < (int)all_pages; i += step) {
+    const int q = find_start(s_page, R, (int)i);
+    a.table[q * a.stride + s_held[q] + (i - s_page[q])] = i < a.n_free ? a.free_pages[i] : -1;
   }
 }
 
 // ------------------------------------------------------- query/key norm and rotation ----
 //
-// L lanes hold one head, eight channels (16 bytes) each; the mean square is an L-lane butterfly,
-// the partner of a channel pair comes from the same lane (interleaved) or by a shuffle from the
-// lane rot/16 further on (halves).  The row's angles are formed once per CTA (fp64 product and
-// reduction to one turn, then sincospi in fp32) while the first heads are in flight.
+// L lanes hold one head, eight channels (16 bytes) each; the mean square is an L-lane butterfly, the
+// partner of a channel comes from the same lane (interleaved) or by a shuffle of the packed values
+// from the lane rot/16 further on (halves).  A warp takes up to `per` heads of one row, all queries'
+// or all keys', so that what a lane multiplies with stays in its registers: out = y cos' + y' sin',
+// y the scaled channel, y' its partner, cos' = gain cos, sin' = partner's gain times +-sin.  The
+// heads come through a ring in shared memory, kDepth asynchronous copies of 512 bytes ahead of
+// their use and the first of them while the angles are formed: in registers as many would leave
+// room for half the warps.
+//
+// Angles: positions reach 2^31, where a product in 32 bits has lost the fraction of a turn and one
+// in fp64 is slow on this part.  So the frequency is taken in turns as a 64-bit binary fraction,
+// inv_freq / (2 pi) = M 2^E C with M the 24-bit significand and C = 1 / (2 pi) to 64 bits; the
+// position times that, modulo 2^64, is the angle's fraction of a turn, exact to 2^-33 of one.
+__device__ __forceinline__ float half_turns(int pos, float freq) {  // angle / pi, in [-1, 1)
+  const uint32_t u = __float_as_uint(freq);
+  const int e = (int)(u >> 23 & 255);
+  if (e > 127 + 20 || (u >> 31)) {  // (large, negative or not a number)
+    double turn = (double)pos * (double)freq * 0.15915494309189533577;
+    turn -= rint(turn);
+    return 2.f * (float)turn;
+  }
+  const uint64_t C = 0x28BE60DB9391054Aull, M = (u & 0x7FFFFFu) | 0x800000u;  // freq = M 2^(e - 150)
+  const uint64_t lo = M * C, hi = __umul64hi(M, C);
+  const int s = 150 - e;  // 3 .. 150; subnormal frequencies turn nothing
+  const uint64_t f = s >= 128 ? 0 : s >= 64 ? hi >> (s - 64) : (hi << (64 - s)) | (lo >> s);
+  const int64_t t = (int64_t)((uint64_t)(int64_t)pos * f);
+  return (float)(int32_t)(t >> 32) * 4.656612873077392578125e-10f;  // 2^-31
+}
+
 template <int L>
-__global__ void __launch_bounds__(256) k_qk_norm_rope(const RopeArgs a, int chunks, int per) {
-  __shared__ float s_cos[128], s_sin[128];
-  const int tid = threadIdx.x, li = tid % L, gi = tid / L;
-  constexpr int kHeads = 256 / L;
-  const int t = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int heads = a.hq + a.hk;
-  const int h0 = chunk * per * kHeads, h1 = min(heads, h0 + per * kHeads);
-  const bool act = li < a.D / 8;
-  const int half = a.rot / 2;
+__global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int qparts, int kparts, int perq,
+                                                         int perk, int blocks) {
+  constexpr int G = 32 / L, kDepth = 8;
+  __shared__ __align__(16) float s_cos[8][128], s_sin[8][128];  // [warp][rot / 2], or one for all
+  __shared__ uint4 s_ring[8][kDepth][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % L, gi = lane / L;
+  // `blocks` CTAs to a row, which form its angles together, or (0) each warp for itself
+  const int parts = qparts + kparts, w = blockIdx.x * 8 + warp;
+  const int row = blocks ? blockIdx.x / blocks : w / parts;
+  const int part = blocks ? w - row * blocks * 8 : w - row * parts;
   mtail::pdl_trigger();
   mtail::pdl_wait();
+  if (row >= a.rows) return;  // (the whole CTA where it works together)
+  const bool isq = part < qparts, act = li < a.D / 8;
+  const int per = isq ? perq : perk, h0 = (isq ? part : part - qparts) * per;
+  const int n = part < parts ? min(per, (isq ? a.hq : a.hk) - h0) : 0;
+  const uint16_t* in = (isq ? a.q + row * a.ldq : a.k + row * a.ldk) + (int64_t)h0 * a.D + 8 * li;
+  uint16_t* out = (isq ? a.qo + row * a.ldqo : a.ko + row * a.ldko) + (int64_t)h0 * a.D + 8 * li;
+  const uint16_t* gain = isq ? a.gq : a.gk;
 
-  auto src = [&](int h) -> const uint4* {
-    return reinterpret_cast<const uint4*>(h < a.hq ? a.q + t * a.ldq + (int64_t)h * a.D
-                                                   : a.k + t * a.ldk + (int64_t)(h - a.hq) * a.D) + li;
-  };
-  int h = h0 + gi;
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (h < h1 && act) u = *src(h);
-
-  if (tid < half) {
-    double turn = (double)a.pos[t] * (double)a.freq[tid] * 0.15915494309189533577;
-    turn -= rint(turn);
-    sincospif(2.f * (float)turn, &s_sin[tid], &s_cos[tid]);
+  const int half = a.rot / 2, hv = a.rot / 16;  // vectors of one half
+  const bool low = li < hv, turns = a.interleaved ? 8 * li < a.rot : li < 2 * hv;
+  const int other = a.interleaved ? li : low ? li + hv : li < 2 * hv ? li - hv : li;
+  const float inv_d = 1.f / (float)a.D;
+  // All loads set out before anything waits for one.
+  const int pos = half ? a.pos[row] : 0;  // (without a rotation there may be no positions)
+  const int first = blocks ? threadIdx.x : lane, step = blocks ? 256 : 32;
+  float* const cosines = s_cos[blocks ? 0 : warp];
+  float* const sines = s_sin[blocks ? 0 : warp];
+  float freq[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) freq[j] = first + j * step < half ? a.freq[first + j * step] : 0.f;
+  const uint32_t one2 = 0x3F803F80;
+  uint4 ug = make_uint4(one2, one2, one2, one2), ugo = ug;
+  if (gain && act && n > 0) {
+    ug = *(reinterpret_cast<const uint4*>(gain) + li);
+    ugo = *(reinterpret_cast<const uint4*>(gain) + other);
   }
-  __syncthreads();
+  uint4(*ring)[32] = s_ring[warp];
+  auto fetch = [&](int v) {  // (a group of copies for each v, empty behind the last)
+    const int i = v * G + gi;
+    if (i < n && act) cp_async16(&ring[v % kDepth][lane], in + i * a.D);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int v = 0; v < kDepth; ++v) fetch(v);
 
-  for (int i = 0; i < per; ++i) {
-    if (h0 + i * kHeads >= h1) break;  // (uniform over the CTA)
-    const int hn = h + kHeads;
-    uint4 un = make_uint4(0, 0, 0, 0);
-    if (i + 1 < per && hn < h1 && act) un = *src(hn);
-    float x[8];
+  float c[8], s[8];  // cos', sin'
+  {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int x = first + j * step;
+      if (x < half) sincospif(half_turns(pos, freq[j]), &sines[x], &cosines[x]);
+    }
+    float g[8], go[8];
+    unpack8(ug, g);
+    unpack8(ugo, go);
+    if (blocks) __syncthreads();
+    else __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = g[e], s[e] = 0.f;
+      if (turns) {
+        const int f = a.interleaved ? 4 * li + e / 2 : 8 * (low ? li : other) + e;
+        const bool front = a.interleaved ? e % 2 == 0 : low;
+        c[e] = g[e] * cosines[f];
+        s[e] = (a.interleaved ? g[e ^ 1] : go[e]) * (front ? -sines[f] : sines[f]);
+      }
+    }
+  }
+  for (int v = 0; v * G < n; ++v) {  // (uniform over the warp)
+    const int i = v * G + gi;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    __syncwarp();
+    const uint4 u = act && i < n ? ring[v % kDepth][lane] : make_uint4(0, 0, 0, 0);
+    float x[8], y[8];
     unpack8(u, x);
-    const bool isq = h < a.hq;
-    const uint16_t* gp = isq ? a.gq : a.gk;
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
-    if (gp && act) {
-      float g[8];
-      unpack8(*(reinterpret_cast<const uint4*>(gp) + li), g);
-      const float rs = rsqrtf(ss / (float)a.D + a.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * rs * g[e];
-    }
     if (a.interleaved) {
-      if (8 * li < a.rot) {
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float c = s_cos[4 * li + e / 2], s = s_sin[4 * li + e / 2];
-          const float lo = x[e], hi = x[e + 1];
-          x[e] = lo * c - hi * s;
-          x[e + 1] = hi * c + lo * s;
-        }
-      }
-    } else if (a.rot) {
-      const int hv = a.rot / 16;  // vectors of one half
-      const bool low = li < hv;
-      const int other = low ? li + hv : li < 2 * hv ? li - hv : li;
+      for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+    } else {
+      unpack8(ring[v % kDepth][gi * L + other], y);  // (used where it turns)
+    }
+    __syncwarp();
+    fetch(v + kDepth);
+    float rs = 1.f;
+    if (gain) {
+      float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = __shfl_sync(0xffffffffu, x[e], other, L);
-        if (li < 2 * hv) {
-          const int f = 8 * (low ? li : other) + e;
-          const float c = s_cos[f], s = s_sin[f];
-          x[e] = low ? x[e] * c - y * s : x[e] * c + y * s;
-        }
-      }
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
+      rs = rsqrtf(fmaf(ss, inv_d, a.eps));
     }
-    if (h < h1 && act) {
-      uint16_t* o = isq ? a.qo + t * a.ldqo + (int64_t)h * a.D
-                        : a.ko + t * a.ldko + (int64_t)(h - a.hq) * a.D;
-      reinterpret_cast<uint4*>(o)[li] = pack8(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = x[e] * rs * c[e];
+      if (turns) x[e] = fmaf(y[e] * rs, s[e], x[e]);  // (else nothing of the partner: it may be infinite)
     }
-    u = un;
-    h = hn;
+    if (i < n && act) *reinterpret_cast<uint4*>(out + i * a.D) = pack8(x);
   }
 }
 
 // ------------------------------------------------------------------------- cache rows ----
 //
-// D/8 lanes hold one token's head, eight channels each, so that a block of 32 channels is four
-// neighbouring lanes: its largest magnitude is two shuffles, and a lane's eight codes are one
-// word.  blockIdx.y = 0: keys, 1: values.
+// D/8 lanes hold one token's head, eight channels each, of its keys and of its values, so that a
+// block of 32 channels is four neighbouring lanes: its largest magnitude is two shuffles, and a
+// lane's eight codes are one word.
 
 template <int D>
 __device__ __forceinline__ uint8_t* tile_of(const RowsArgs& a, int64_t slot, int h) {
-  const int64_t page = slot / a.page;
+  // slot / page by the multiplier 2^64 / page, rounded up (slot * page < 2^64)
+  const int64_t page = (int64_t)__umul64hi((uint64_t)slot, a.page_magic);
   const int off = (int)(slot - page * a.page);
   return a.cache + ((page * a.heads + h) * (a.page / 16) + off / 16) * (17 * D);
 }
 // byte n of lane l of a tile's codes
 __device__ __forceinline__ int lane_byte(int n, int l) { return (n >> 4) * 512 + l * 16 + (n & 15); }
 
-template <int D>
-__global__ void __launch_bounds__(256) k_kv4_append(const RowsArgs a) {
-  constexpr int L = D / 8, NB = D / 32;
-  const bool val = blockIdx.y != 0;
-  const int64_t id = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;  // (row, head)
-  const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
-  const bool in = id < (int64_t)a.rows * a.heads;
-  const int row = in ? (int)(id / a.heads) : 0, h = in ? (int)(id % a.heads) : 0;
-  mtail::pdl_trigger();
-  mtail::pdl_wait();
-  int64_t slot = in ? a.slots[row] : -1;
-  if (slot >= a.n_slots) {
-    if (h == 0 && i == 0 && !val) report(a.status, kStatusBadSlot);
-    slot = -1;
-  }
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (slot >= 0) {
-    const uint16_t* p = val ? a.v + row * a.ldv : a.k + row * a.ldk;
-    u = *(reinterpret_cast<const uint4*>(p + h * D) + i);
-  }
-  float x[8];
-  unpack8(u, x);
+// Eight bf16 of a block's four lanes -> this lane's codes and the block's scale byte.
+__device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t* scale) {
   // the block's largest magnitude as bf16 bits: an infinity or a NaN (exponent 255) is larger
   // than every number
-  uint32_t am = 0;
-  am = max(max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu), max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu));
-  am = max(am, max(max(u.z & 0x7FFFu, (u.z >> 16) & 0x7FFFu),
-                   max(u.w & 0x7FFFu, (u.w >> 16) & 0x7FFFu)));
+  uint32_t am = max(max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu), max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu));
+  am = max(am, max(max(u.z & 0x7FFFu, (u.z >> 16) & 0x7FFFu), max(u.w & 0x7FFFu, (u.w >> 16) & 0x7FFFu)));
   am = max(am, __shfl_xor_sync(~0u, am, 1));
   am = max(am, __shfl_xor_sync(~0u, am, 2));
-  uint32_t sc, w;
   if (am >= 0x7F80u) {
-    sc = 255;
-    w = 0;
-  } else {
-    // smallest e in [-126, 125] with amax <= 6 * 2^e: amax = 1.m * 2^E, 6 = 1.5 * 2^2
-    const int e = min(max((int)(am >> 7) - 129 + ((am & 0x7Fu) > 0x40u ? 1 : 0), -126), 125);
-    sc = (uint32_t)(e + 127);
-    const float inv = mtail::exp2_int(-e);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= inv;
-    w = mtail::e2m1x8_pack(x);
+    *scale = 255;
+    return 0;
   }
-  const int t = (int)(slot & 15);  // (a page is a multiple of 16 tokens)
-  uint8_t* tile = slot >= 0 ? tile_of<D>(a, slot, h) : nullptr;
-  if (!val) {
-    if (slot >= 0)
-      *reinterpret_cast<uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c)) = w;
-    // the scale bytes of up to four blocks in one store
-    uint32_t sw = sc << (8 * (b & 3));
-    sw |= __shfl_xor_sync(~0u, sw, 4);
-    if (NB > 2) sw |= __shfl_xor_sync(~0u, sw, 8);
-    uint8_t* s = tile + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
-    if (slot >= 0 && c == 0 && (b & 3) == 0) {
-      if (NB == 2)
-        *reinterpret_cast<uint16_t*>(s) = (uint16_t)sw;
-      else
-        *reinterpret_cast<uint32_t*>(s + b) = sw;
-    }
-  } else {
-    // lanes (b, c), b = 0, 1 collect the 16-bit pieces of every block for g = 2c + b
-    uint32_t vv[NB / 2];
+  // smallest e in [-126, 125] with amax <= 6 * 2^e: amax = 1.m * 2^E, 6 = 1.5 * 2^2
+  const int e = min(max((int)(am >> 7) - 129 + ((am & 0x7Fu) > 0x40u ? 1 : 0), -126), 125);
+  *scale = (uint32_t)(e + 127);
+  const float inv = mtail::exp2_int(-e);
+  float x[8];
+  unpack8(u, x);
 #pragma unroll
-    for (int k = 0; k < NB / 2; ++k) {
-      const uint32_t w0 = __shfl_sync(~0u, w, 8 * k + c, L), w1 = __shfl_sync(~0u, w, 8 * k + 4 + c, L);
-      vv[k] = b == 0 ? __byte_perm(w0, w1, 0x5410) : __byte_perm(w0, w1, 0x7632);
-    }
-    if (slot >= 0 && b < 2) {
-      uint8_t* p = tile + 8 * D +
-                   lane_byte(((t >> 3) * 2 + (t & 1)) * (D / 16), (2 * c + b) * 4 + ((t & 7) >> 1));
-      if (NB == 2) *reinterpret_cast<uint32_t*>(p) = vv[0];
-      else if (NB == 4) *reinterpret_cast<uint2*>(p) = make_uint2(vv[0], vv[NB / 2 - 1]);
-      else *reinterpret_cast<uint4*>(p) = make_uint4(vv[0], vv[1 % (NB / 2)], vv[2 % (NB / 2)], vv[3 % (NB / 2)]);
-    }
-    if (slot >= 0 && c == 0)
-      tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)] = (uint8_t)sc;
-  }
+  for (int j = 0; j < 8; ++j) x[j] *= inv;
+  return mtail::e2m1x8_pack(x);
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
+__global__ void __launch_bounds__(256) k_kv4_append(const RowsArgs a) {
   constexpr int L = D / 8, NB = D / 32;
-  const bool val = blockIdx.y != 0;
-  const int64_t id = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const uint32_t id = blockIdx.x * (256 / L) + threadIdx.x / L;  // (row, head); at most 2^32
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
   mtail::pdl_trigger();
   mtail::pdl_wait();
-  if (id >= (int64_t)a.rows * a.heads) return;
-  const int row = (int)(id / a.heads), h = (int)(id % a.heads);
-  const int64_t slot = a.slots[row];
-  if (slot < 0 || slot >= a.n_slots) {
-    if (slot >= 0 && h == 0 && i == 0 && !val) report(a.status, kStatusBadSlot);
-    return;
+  const uint32_t row = id / (uint32_t)a.heads, h = id - row * (uint32_t)a.heads;
+  int64_t slot = -1;
+  uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+  if (row < (uint32_t)a.rows) {  // (the loads need not wait for the slot)
+    slot = a.slots[row];
+    ku = *(reinterpret_cast<const uint4*>(a.k + row * a.ldk + h * D) + i);
+    vu = *(reinterpret_cast<const uint4*>(a.v + row * a.ldv + h * D) + i);
   }
-  const int t = (int)(slot & 15);
-  const uint8_t* tile = tile_of<D>(a, slot, h);
-  uint32_t w, s;
-  if (!val) {
-    w = *reinterpret_cast<const uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c));
-    s = tile[16 * D + (t & 7) * (D / 16) + (t >> 3) * NB + b];
-  } else {
-    const uint8_t* p = tile + 8 * D;
-    const int n = ((t >> 3) * 2 + (t & 1)) * (D / 16) + 2 * b;
-    w = *reinterpret_cast<const uint16_t*>(p + lane_byte(n, 8 * c + ((t & 7) >> 1)));
-    w |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + lane_byte(n, 8 * c + 4 + ((t & 7) >> 1))) << 16;
-    s = tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)];
+  if (slot >= a.n_slots) {
+    if (h == 0 && i == 0) report(a.status, kStatusBadSlot);
+    slot = -1;
   }
+  uint32_t ks, vs;
+  const uint32_t kw = quantize8(ku, &ks), vw = quantize8(vu, &vs);
+  // the key scales of up to four blocks in one store
+  uint32_t sw = ks << (8 * (b & 3));
+  sw |= __shfl_xor_sync(~0u, sw, 4);
+  if (NB > 2) sw |= __shfl_xor_sync(~0u, sw, 8);
+  // lanes (b, c), b = 0, 1 collect the 16-bit pieces of every block of the values for g = 2c + b
+  uint32_t vv[4];
+#pragma unroll
+  for (int k = 0; k < NB / 2; ++k) {
+    const uint32_t w0 = __shfl_sync(~0u, vw, 8 * k + c, L), w1 = __shfl_sync(~0u, vw, 8 * k + 4 + c, L);
+    vv[k] = b == 0 ? __byte_perm(w0, w1, 0x5410) : __byte_perm(w0, w1, 0x7632);
+  }
+  if (slot < 0) return;
+  const int t = (int)(slot & 15);  // (a page is a multiple of 16 tokens)
+  uint8_t* tile = tile_of<D>(a, slot, (int)h);
+  *reinterpret_cast<uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c)) = kw;
+  if (c == 0 && (b & 3) == 0) {
+    uint8_t* s = tile + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
+    if (NB == 2) *reinterpret_cast<uint16_t*>(s) = (uint16_t)sw;
+    else *reinterpret_cast<uint32_t*>(s + b) = sw;
+  }
+  if (b < 2) {
+    uint8_t* p = tile + 8 * D +
+                 lane_byte(((t >> 3) * 2 + (t & 1)) * (D / 16), (2 * c + b) * 4 + ((t & 7) >> 1));
+    if constexpr (NB == 2) *reinterpret_cast<uint32_t*>(p) = vv[0];
+    else if constexpr (NB == 4) *reinterpret_cast<uint2*>(p) = make_uint2(vv[0], vv[1]);
+    else *reinterpret_cast<uint4*>(p) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
+  }
+  if (c == 0) tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)] = (uint8_t)vs;
+}
+
+__device__ __forceinline__ uint4 dequantize8(uint32_t w, uint32_t s) {
   const float f = s == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23);  // (0: 0)
   uint32_t hh[4];
   mtail::e2m1x8_to_f16x2(w, hh[0], hh[1], hh[2], hh[3]);
@@ -358,42 +384,91 @@ __global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
     x[2 * j] = v.x * f;
     x[2 * j + 1] = v.y * f;
   }
-  uint16_t* o = val ? a.v + row * a.ldv : a.k + row * a.ldk;
-  *(reinterpret_cast<uint4*>(o + h * D) + i) = pack8(x);
+  return pack8(x);
+}
+
+// Two (row, head) pairs per group of lanes: their look-ups overlap.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
+  constexpr int L = D / 8, NB = D / 32, kPairs = 2;
+  const uint32_t id0 = blockIdx.x * (kPairs * 256 / L) + threadIdx.x / L;
+  const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
+  mtail::pdl_trigger();
+  mtail::pdl_wait();
+  uint32_t row[kPairs], h[kPairs], kw[kPairs], vw[kPairs], ks[kPairs], vs[kPairs];
+  int64_t slot[kPairs];
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    const uint32_t id = id0 + p * (256 / L);
+    row[p] = id / (uint32_t)a.heads, h[p] = id - row[p] * (uint32_t)a.heads;
+    slot[p] = row[p] < (uint32_t)a.rows ? a.slots[row[p]] : -1;
+  }
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    if (slot[p] >= a.n_slots) {
+      if (h[p] == 0 && i == 0) report(a.status, kStatusBadSlot);
+      slot[p] = -1;
+    }
+    if (slot[p] < 0) continue;
+    const int t = (int)(slot[p] & 15);
+    const uint8_t* tile = tile_of<D>(a, slot[p], (int)h[p]);
+    kw[p] = *reinterpret_cast<const uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c));
+    ks[p] = tile[16 * D + (t & 7) * (D / 16) + (t >> 3) * NB + b];
+    const uint8_t* v = tile + 8 * D;
+    const int n = ((t >> 3) * 2 + (t & 1)) * (D / 16) + 2 * b;
+    vw[p] = *reinterpret_cast<const uint16_t*>(v + lane_byte(n, 8 * c + ((t & 7) >> 1))) |
+            (uint32_t)*reinterpret_cast<const uint16_t*>(v + lane_byte(n, 8 * c + 4 + ((t & 7) >> 1))) << 16;
+    vs[p] = tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)];
+  }
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    if (slot[p] < 0) continue;
+    *(reinterpret_cast<uint4*>(a.k + row[p] * a.ldk + h[p] * D) + i) = dequantize8(kw[p], ks[p]);
+    *(reinterpret_cast<uint4*>(a.v + row[p] * a.ldv + h[p] * D) + i) = dequantize8(vw[p], vs[p]);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_step_tables(const TablesArgs& a, cudaStream_t st) {
   const int threads = std::max(128, (a.reqs + 31) / 32 * 32);
-  // four rows a thread, at most two CTAs' worth of threads on every SM
-  const int64_t want = ((int64_t)a.max_rows + 4 * threads - 1) / (4 * threads);
-  const int grid = (int)std::min<int64_t>(want, 2 * num_sms());
+  // One row a thread while that fills the GPU once: the rows' loads are what takes time.
+  const int want = (a.max_rows + threads - 1) / threads;
+  const int grid = std::min(want, num_sms() * std::max(1, 2048 / threads));
   return mtail::launch_k(k_step_tables, dim3(grid), dim3(threads), 0, st, true, a);
 }
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
-  const int L = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
-  const int kHeads = 256 / L, groups = (a.hq + a.hk + kHeads - 1) / kHeads;
-  // one group of heads per CTA until the rows alone fill the GPU several times over
-  int per = (int)std::min<int64_t>(groups, std::max<int64_t>(1, (int64_t)a.rows * groups / (num_sms() * 16)));
-  const int chunks = (groups + per - 1) / per;
-  const int64_t grid = (int64_t)a.rows * chunks;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int L = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, G = 32 / L;
+  // One head per lane group and warp until every SM has 48 warps, then up to 16, in equal parts: the
+  // angles are formed once per warp, and a ring is better used by a longer run (8192 rows of 64 + 8
+  // heads: 60 us with 16, 65 with 8).
+  const int64_t groups = (int64_t)a.rows * ((a.hq + a.hk + G - 1) / G), fill = (int64_t)num_sms() * 48;
+  const int most = G * (int)std::min<int64_t>(std::max<int64_t>(groups / fill, 1), 16);
+  auto split = [&](int heads, int& parts) {
+    parts = (heads + most - 1) / most;
+    return parts ? ((heads + parts - 1) / parts + G - 1) / G * G : G;
+  };
+  int qparts, kparts;
+  const int perq = split(a.hq, qparts), perk = split(a.hk, kparts);
+  // With one head to a lane group the angles are a warp's longest work: there the CTAs take whole
+  // rows and form them together (32 rows, D 256: 2.9 us against 3.3).
+  const int blocks = most == G ? (qparts + kparts + 7) / 8 : 0;
+  const int64_t grid = blocks ? (int64_t)a.rows * blocks : ((int64_t)a.rows * (qparts + kparts) + 7) / 8;
+  if (grid > INT32_MAX / 8) return cudaErrorInvalidConfiguration;
   auto* kernel = L == 8 ? k_qk_norm_rope<8> : L == 16 ? k_qk_norm_rope<16> : k_qk_norm_rope<32>;
-  return mtail::launch_k(kernel, dim3((unsigned)grid), dim3(256), 0, st, true, a, chunks, per);
+  return mtail::launch_k(kernel, dim3((unsigned)grid), dim3(256), 0, st, true, a, qparts, kparts, perq, perk, blocks);
 }
 
 namespace {
 template <bool kAppend>
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
-  const int per = 256 / (a.D / 8);
+  const int per = 256 / (a.D / 8) * (kAppend ? 1 : 2);            // (row, head) pairs of a CTA
   const int64_t n = ((int64_t)a.rows * a.heads + per - 1) / per;  // <= 2^24 * 256 / 8
-  const dim3 grid((unsigned)n, 2);
   auto* kernel = a.D == 64    ? (kAppend ? k_kv4_append<64> : k_kv4_read<64>)
                  : a.D == 128 ? (kAppend ? k_kv4_append<128> : k_kv4_read<128>)
                               : (kAppend ? k_kv4_append<256> : k_kv4_read<256>);
-  return mtail::launch_k(kernel, grid, dim3(256), 0, st, true, a);
+  return mtail::launch_k(kernel, dim3((unsigned)n), dim3(256), 0, st, true, a);
 }
 }  // namespace
 
