@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
 
 template <int D>
 __device__ __forceinline__ uint8_t* tile_of(const RowsArgs& a, int64_t slot, int h) {
-  // slot / page by the multiplier 2^64 / page, rounded up (slot * page < 2^64)
+  // slot / page by the multiplier 2^64 / page, rounded up: exact while slot * page < 2^64
   const int64_t page = (int64_t)__umul64hi((uint64_t)slot, a.page_magic);
   const int off = (int)(slot - page * a.page);
   return a.cache + ((page * a.heads + h) * (a.page / 16) + off / 16) * (17 * D);
@@ -322,55 +322,66 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t* scale) {
   return mtail::e2m1x8_pack(x);
 }
 
-template <int D>
+// kPairs (row, head) pairs per group of lanes, here and in the read: their loads overlap.
+template <int D, int kPairs>
 __global__ void __launch_bounds__(256) k_kv4_append(const RowsArgs a) {
   constexpr int L = D / 8, NB = D / 32;
-  const uint32_t id = blockIdx.x * (256 / L) + threadIdx.x / L;  // (row, head); at most 2^32
+  const uint32_t id0 = blockIdx.x * (kPairs * 256 / L) + threadIdx.x / L;  // (row, head); at most 2^32
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
   mtail::pdl_trigger();
   mtail::pdl_wait();
-  const uint32_t row = id / (uint32_t)a.heads, h = id - row * (uint32_t)a.heads;
-  int64_t slot = -1;
-  uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-  if (row < (uint32_t)a.rows) {  // (the loads need not wait for the slot)
-    slot = a.slots[row];
-    ku = *(reinterpret_cast<const uint4*>(a.k + row * a.ldk + h * D) + i);
-    vu = *(reinterpret_cast<const uint4*>(a.v + row * a.ldv + h * D) + i);
-  }
-  if (slot >= a.n_slots) {
-    if (h == 0 && i == 0) report(a.status, kStatusBadSlot);
-    slot = -1;
-  }
-  uint32_t ks, vs;
-  const uint32_t kw = quantize8(ku, &ks), vw = quantize8(vu, &vs);
-  // the key scales of up to four blocks in one store
-  uint32_t sw = ks << (8 * (b & 3));
-  sw |= __shfl_xor_sync(~0u, sw, 4);
-  if (NB > 2) sw |= __shfl_xor_sync(~0u, sw, 8);
-  // lanes (b, c), b = 0, 1 collect the 16-bit pieces of every block of the values for g = 2c + b
-  uint32_t vv[4];
+  uint32_t h[kPairs];
+  int64_t slot[kPairs];
+  uint4 ku[kPairs], vu[kPairs];
 #pragma unroll
-  for (int k = 0; k < NB / 2; ++k) {
-    const uint32_t w0 = __shfl_sync(~0u, vw, 8 * k + c, L), w1 = __shfl_sync(~0u, vw, 8 * k + 4 + c, L);
-    vv[k] = b == 0 ? __byte_perm(w0, w1, 0x5410) : __byte_perm(w0, w1, 0x7632);
+  for (int p = 0; p < kPairs; ++p) {
+    const uint32_t id = id0 + p * (256 / L), row = id / (uint32_t)a.heads;
+    h[p] = id - row * (uint32_t)a.heads;
+    slot[p] = -1;
+    ku[p] = vu[p] = make_uint4(0, 0, 0, 0);
+    if (row < (uint32_t)a.rows) {  // (the loads need not wait for the slot)
+      slot[p] = a.slots[row];
+      ku[p] = *(reinterpret_cast<const uint4*>(a.k + row * a.ldk + h[p] * D) + i);
+      vu[p] = *(reinterpret_cast<const uint4*>(a.v + row * a.ldv + h[p] * D) + i);
+    }
   }
-  if (slot < 0) return;
-  const int t = (int)(slot & 15);  // (a page is a multiple of 16 tokens)
-  uint8_t* tile = tile_of<D>(a, slot, (int)h);
-  *reinterpret_cast<uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c)) = kw;
-  if (c == 0 && (b & 3) == 0) {
-    uint8_t* s = tile + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
-    if (NB == 2) *reinterpret_cast<uint16_t*>(s) = (uint16_t)sw;
-    else *reinterpret_cast<uint32_t*>(s + b) = sw;
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    if (slot[p] >= a.n_slots) {
+      if (h[p] == 0 && i == 0) report(a.status, kStatusBadSlot);
+      slot[p] = -1;
+    }
+    uint32_t ks, vs;
+    const uint32_t kw = quantize8(ku[p], &ks), vw = quantize8(vu[p], &vs);
+    // the key scales of up to four blocks in one store
+    uint32_t sw = ks << (8 * (b & 3));
+    sw |= __shfl_xor_sync(~0u, sw, 4);
+    if (NB > 2) sw |= __shfl_xor_sync(~0u, sw, 8);
+    // lanes (b, c), b = 0, 1 collect the 16-bit pieces of every block of the values for g = 2c + b
+    uint32_t vv[4];
+#pragma unroll
+    for (int k = 0; k < NB / 2; ++k) {
+      const uint32_t w0 = __shfl_sync(~0u, vw, 8 * k + c, L), w1 = __shfl_sync(~0u, vw, 8 * k + 4 + c, L);
+      vv[k] = b == 0 ? __byte_perm(w0, w1, 0x5410) : __byte_perm(w0, w1, 0x7632);
+    }
+    if (slot[p] < 0) continue;  // (before the next pair's shuffles the warp is together again)
+    const int t = (int)(slot[p] & 15);  // (a page is a multiple of 16 tokens)
+    uint8_t* tile = tile_of<D>(a, slot[p], (int)h[p]);
+    *reinterpret_cast<uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c)) = kw;
+    if (c == 0 && (b & 3) == 0) {
+      uint8_t* s = tile + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
+      if (NB == 2) *reinterpret_cast<uint16_t*>(s) = (uint16_t)sw;
+      else *reinterpret_cast<uint32_t*>(s + b) = sw;
+    }
+    if (b < 2) {
+      uint8_t* q = tile + 8 * D +
+                   lane_byte(((t >> 3) * 2 + (t & 1)) * (D / 16), (2 * c + b) * 4 + ((t & 7) >> 1));
+      if constexpr (NB == 2) *reinterpret_cast<uint32_t*>(q) = vv[0];
+      else if constexpr (NB == 4) *reinterpret_cast<uint2*>(q) = make_uint2(vv[0], vv[1]);
+      else *reinterpret_cast<uint4*>(q) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
+    }
+    if (c == 0) tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)] = (uint8_t)vs;
   }
-  if (b < 2) {
-    uint8_t* p = tile + 8 * D +
-                 lane_byte(((t >> 3) * 2 + (t & 1)) * (D / 16), (2 * c + b) * 4 + ((t & 7) >> 1));
-    if constexpr (NB == 2) *reinterpret_cast<uint32_t*>(p) = vv[0];
-    else if constexpr (NB == 4) *reinterpret_cast<uint2*>(p) = make_uint2(vv[0], vv[1]);
-    else *reinterpret_cast<uint4*>(p) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
-  }
-  if (c == 0) tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)] = (uint8_t)vs;
 }
 
 __device__ __forceinline__ uint4 dequantize8(uint32_t w, uint32_t s) {
@@ -387,10 +398,9 @@ __device__ __forceinline__ uint4 dequantize8(uint32_t w, uint32_t s) {
   return pack8(x);
 }
 
-// Two (row, head) pairs per group of lanes: their look-ups overlap.
-template <int D>
+template <int D, int kPairs>
 __global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
-  constexpr int L = D / 8, NB = D / 32, kPairs = 2;
+  constexpr int L = D / 8, NB = D / 32;
   const uint32_t id0 = blockIdx.x * (kPairs * 256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
   mtail::pdl_trigger();
@@ -461,14 +471,21 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
 }
 
 namespace {
+template <bool kAppend, int kPairs>
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
+  const int per = kPairs * 256 / (a.D / 8);                       // pairs of a CTA
+  const int64_t n = ((int64_t)a.rows * a.heads + per - 1) / per;  // <= 2^24 * 256 / 8
+  auto* kernel = a.D == 64    ? (kAppend ? k_kv4_append<64, kPairs> : k_kv4_read<64, kPairs>)
+                 : a.D == 128 ? (kAppend ? k_kv4_append<128, kPairs> : k_kv4_read<128, kPairs>)
+                              : (kAppend ? k_kv4_append<256, kPairs> : k_kv4_read<256, kPairs>);
+  return mtail::launch_k(kernel, dim3((unsigned)n), dim3(256), 0, st, true, a);
+}
 template <bool kAppend>
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
-  const int per = 256 / (a.D / 8) * (kAppend ? 1 : 2);            // (row, head) pairs of a CTA
-  const int64_t n = ((int64_t)a.rows * a.heads + per - 1) / per;  // <= 2^24 * 256 / 8
-  auto* kernel = a.D == 64    ? (kAppend ? k_kv4_append<64> : k_kv4_read<64>)
-                 : a.D == 128 ? (kAppend ? k_kv4_append<128> : k_kv4_read<128>)
-                              : (kAppend ? k_kv4_append<256> : k_kv4_read<256>);
-  return mtail::launch_k(kernel, dim3((unsigned)n), dim3(256), 0, st, true, a);
+  // One pair a group of lanes until the GPU is filled several times over (32 rows of 8 heads, in and
+  // out: 3.6 us, with two 4.5), then two (65537 rows: 134 us, with one 144).
+  const int64_t threads = (int64_t)a.rows * a.heads * (a.D / 8);
+  return threads < (int64_t)num_sms() * 2048 * 4 ? launch_rows<kAppend, 1>(a, st) : launch_rows<kAppend, 2>(a, st);
 }
 }  // namespace
 

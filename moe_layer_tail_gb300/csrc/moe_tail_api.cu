@@ -875,7 +875,7 @@ extern "C" int moe_kv4_attention(int32_t rows, int32_t reqs, int32_t q_heads, in
   const void* need[] = {q, cache, out, workspace};
   for (const void* p : need)
     if (!p || !aligned16(p)) return MOE_TAIL_ERR_INVALID_ARG;
-  if (!block_table || !row_starts || !kv_lens) return MOE_TAIL_ERR_INVALID_ARG;
+  if (!block_table || !row_starts || !kv_lens || out == q) return MOE_TAIL_ERR_INVALID_ARG;
   const int64_t wq = (int64_t)q_heads * head_dim;
   if (!row_stride_ok(ld_q, wq) || !row_stride_ok(ld_o, wq)) return MOE_TAIL_ERR_INVALID_ARG;
   kv4::AttnArgs a;

@@ -150,8 +150,7 @@ def norm_rope(x, gamma, pos, freq, eps, interleaved):
 
 def attention(q, K, V, table, starts, lens, page, scale, window=0, sinks=0):
     """q float64 [T, Hq, D], K, V [pages, heads, page, D] -> {row: (out [Hq, D], avg [Hq, D] =
-    sum p |v| / sum p, spread [Hq] = scale * max_j sum_d |q_d k_jd|, floor [Hq, D] = tokens seen
-    times the largest |v| of the block of 32 channels)}."""
+    sum p |v| / sum p, spread [Hq] = scale * max_j sum_d |q_d k_jd|, total [Hq, D] = sum |v|)}."""
     T, Hq, D = q.shape
     H = K.shape[1]
     G = Hq // H
@@ -163,7 +162,7 @@ def attention(q, K, V, table, starts, lens, page, scale, window=0, sinks=0):
             j = np.arange(0, max(p + 1, 0))
             if window:
                 j = j[(j > p - window) | (j < sinks)]
-            out, avg, spread, floor = np.zeros((Hq, D)), np.zeros((Hq, D)), np.zeros(Hq), np.zeros((Hq, D))
+            out, avg, spread, total = np.zeros((Hq, D)), np.zeros((Hq, D)), np.zeros(Hq), np.zeros((Hq, D))
             j = j[(table[r, j // page] >= 0) & (table[r, j // page] < K.shape[0])]
             if len(j):
                 pg, off = table[r, j // page], j % page
@@ -177,23 +176,23 @@ def attention(q, K, V, table, starts, lens, page, scale, window=0, sinks=0):
                         out[h * G:(h + 1) * G] = w @ v
                         avg[h * G:(h + 1) * G] = w @ np.abs(v)
                     spread[h * G:(h + 1) * G] = (np.abs(qq) @ np.abs(k).T).max(-1) * scale
-                    floor[h * G:(h + 1) * G] = np.repeat(np.abs(v).reshape(
-                        len(j), -1, 32).max((0, 2)), 32) * len(j)
-            res[i] = (out, avg, spread, floor)
+                    total[h * G:(h + 1) * G] = np.abs(v).sum(0)
+            res[i] = (out, avg, spread, total)
     return res
 
 
-def attention_tolerance(out, avg, spread, floor, D):
+def attention_tolerance(out, avg, spread, total, D):
     """|kernel - out| at most: the result's own rounding to bf16 (half a step: 2^-8 of the value);
-    the numerators' rounding to f16 (half a step, 2^-11 of each term, so 2^-11 of sum p |v| /
-    sum p); the fp32 sums of the scores: D / 16 products of 16 terms and D / 32 scaled additions,
-    each off by at most 2^-22 of the terms' magnitudes, in the exponent of numerator and
-    denominator alike (twice); 2^-18 for the exponentials and the output sums (fp32).  Numerators
-    below the f16 normals are rounded in fixed point: a token enters as f16(f16(2^11 p) 2^(s - lo -
-    14)) E2M1, its window's lower end lo at most 10 octaves below the block's largest scale so far,
-    so each of the two roundings (2^-25 at most) moves p v by 6 2^-25 2^(14 - 11) 2^(lo - 127) <=
-    6 2^-32 2^(largest s - 127) <= 2^-30 of the block's largest |v| (a block's largest code is 4 or
-    6: amax > 3 2^s), against a sum of p of 1 at least: 2^-30 max |v| for each token seen."""
-    d = (D / 16 + D / 32) * 2.0 ** -22 * spread[:, None]
-    return (2.0 ** -8 * np.abs(out) + avg * (2.0 ** -11 + 2 * d + 2.0 ** -18) + 2.0 ** -30 * floor
-            + 1e-38)
+    the numerators' rounding to tf32 (half a step, 2^-11 of each term, so 2^-11 of sum p |v| /
+    sum p; the sum of the numerators takes them unrounded); queries and keys enter the score's
+    product exactly (8 and 2 significant bits), its fp32 sums are D / 8 additions of 8 products,
+    each off by at most 2^-22 of the terms' magnitudes (2^-23 for each of alignment and cut), and
+    the scale one more, in the exponent of numerator and denominator alike (twice); the output
+    sums are fp32 additions of 8 tokens each, at most 128 of them in one range here (1024 tokens),
+    2^-23 each: 2^-16 with the exponentials' 2^-22 and the join's few.  Numerators and the join's
+    weights below 2^-126 are flushed to zero, against a sum of 1 at least (a row's reference is at
+    most its maximum): 2 2^-126 |v| of each token; a subnormal result is off by its half step,
+    2^-134."""
+    d = (D / 8 + 1) * 2.0 ** -22 * spread[:, None]
+    return (2.0 ** -8 * np.abs(out) + avg * (2.0 ** -11 + 2 * d + 2.0 ** -16) + 2.0 ** -125 * total
+            + 2.0 ** -134)

@@ -71,6 +71,35 @@ def test_append_and_read(D, heads, page, rows):
     assert int(st) == 0
 
 
+@pytest.mark.parametrize("D,heads", [(64, 1), (64, 5), (128, 3), (256, 2)])
+def test_rows_side_by_side_in_their_tiles(D, heads):
+    # runs of rows as prompts leave them: on and off the tiles' boundaries, over pages, with breaks,
+    # gaps and an end inside a tile; what is not theirs stays
+    rng = np.random.default_rng([D, heads])
+    page, pages = 32, 12
+    runs = [(0, 64), (64 + 5, 40), (200, 3), (211, 4), (250, 1), (256, 27), (300, 37)]
+    slots = np.concatenate([np.arange(a, a + n) for a, n in runs]).astype(np.int64)
+    for skip in ((), (7, 100, 101)):
+        at = slots.copy()
+        at[list(skip)] = -1
+        rows = len(at)
+        k, v = normal_bits(rng, rows, heads, D), normal_bits(rng, rows, heads, D)
+        expect = rng.integers(0, 256, (pages, heads, page // 16, 17 * D), dtype=np.uint8)
+        cache = torch.from_numpy(expect.copy()).cuda()
+        for r in range(rows):
+            if at[r] >= 0:
+                ref.write_row(expect, at[r], k[r], v[r])
+        st = status_word()
+        mt.kv4_append(cache, to_dev(k), to_dev(v), torch.from_numpy(at).cuda(), status=st)
+        assert np.array_equal(cache.cpu().numpy(), expect) and int(st) == 0
+    # a run into the end of the cache: its last rows have no slot
+    at = np.arange(pages * page - 9, pages * page + 3).astype(np.int64)
+    for r in range(9):
+        ref.write_row(expect, at[r], k[r], v[r])
+    mt.kv4_append(cache, to_dev(k)[:12], to_dev(v)[:12], torch.from_numpy(at).cuda(), status=st)
+    assert np.array_equal(cache.cpu().numpy(), expect) and int(st) == mt.KV4_STATUS_BAD_SLOT
+
+
 def test_rows_without_a_slot_are_left_alone():
     rng = np.random.default_rng(1)
     before = rng.integers(0, 256, (2, 2, 1, 17 * 64), dtype=np.uint8)
@@ -166,7 +195,10 @@ def test_step_tables_reports(case):
     (1, 1, 1, 16, 16, False, 100), (1, 128, 8, 128, 128, False, 1 << 20),
     (5, 6, 2, 64, 32, True, 4000), (3, 5, 0, 96, 96, False, 1 << 31),
     (33, 16, 3, 192, 64, False, 1 << 31), (32, 64, 4, 256, 256, True, 1 << 31),
-    (7, 40, 8, 256, 64, False, 1 << 17), (700, 8, 1, 128, 0, False, 10), (9, 3, 3, 112, 16, True, 50)])
+    (7, 40, 8, 256, 64, False, 1 << 17), (700, 8, 1, 128, 0, False, 10), (9, 3, 3, 112, 16, True, 50),
+    # many heads to a warp: one run of a ring and more
+    (3000, 40, 3, 64, 32, True, 1 << 31), (900, 20, 3, 256, 256, False, 1 << 17),
+    (8000, 64, 8, 16, 16, False, 1 << 20), (2500, 33, 7, 48, 32, False, 1 << 10)])
 def test_qk_norm_rope(T, hq, hk, D, rot, inter, far):
     rng = np.random.default_rng([T, hq, D, rot])
     w = (hq + hk) * D
@@ -203,6 +235,10 @@ def test_qk_norm_rope(T, hq, hk, D, rot, inter, far):
     check(qo, slice(0, hq * D), hq, gq)
     if hk:
         check(ko, slice(hq * D, w), hk, gk)
+    if not rot:  # (positions are not needed then)
+        again = torch.empty_like(qo)
+        mt.qk_norm_rope(q, None, to_dev(gq), None, None, None, again, None, eps=eps)
+        assert torch.equal(again, qo)
     # without a query norm, and in place in the packed tensor
     mt.qk_norm_rope(q, k if hk else None, None, to_dev(gk) if hk else None, posd, freqd, q,
                     k if hk else None, eps=eps, interleaved=inter)
@@ -272,8 +308,8 @@ class Step:
         K, V = ref.decode(self.cache)
         want = ref.attention(ref.bf16_to_f64(self.q), K, V, self.table, self.starts, self.lens,
                              self.page, scale or self.D ** -0.5, window, sinks)
-        for i, (out, avg, spread, floor) in want.items():
-            tol = ref.attention_tolerance(out, avg, spread, floor, self.D)
+        for i, (out, avg, spread, total) in want.items():
+            tol = ref.attention_tolerance(out, avg, spread, total, self.D)
             bad = ~(np.abs(got[i] - out) <= tol) & ~(np.isnan(got[i]) & np.isnan(out))
             assert not bad.any(), (i, int(bad.sum()), float(np.nanmax(np.abs(got[i] - out) / tol)))
         assert (got[int(self.starts[-1]):] == 5).all()  # no request's rows: left as they were
@@ -342,6 +378,41 @@ def test_attention_peaked_and_large_queries():
     s.q[3] = 0x0003
     s.check(s.run())
     s.check(s.run(scale=3.0), scale=3.0)
+
+
+@pytest.mark.parametrize("D,G,new", [(64, 16, 2), (128, 8, 1), (128, 16, 1), (128, 40, 1), (256, 16, 1)])
+def test_attention_scores_that_outgrow_the_first_step(D, G, new):
+    # keys that grow (and shrink) by octaves every 128 tokens: the running maximum moves far, in
+    # the first parts of a request as in its later ones
+    _, _, ks, _ = ref.offsets(D)
+    for grow in ((0, 5, 6, 3, 7, 0, 8, 9), (8, 0, 4, 2, 9, 1, 0, 10)):
+        s = Step(30, [900, 260], new, G, 1, D, 16)
+        for r in range(2):
+            for e in range(-(-int(s.lens[r]) // 16)):
+                at = s.cache[s.table[r, e], 0, 0]
+                at[ks] = np.where(at[ks] == 255, 255, np.minimum(at[ks].astype(int) + grow[e // 8], 200))
+        s.check(s.run())
+
+
+def test_attention_rows_that_see_nothing_of_their_first_steps():
+    s = Step(31, [5000, 700], [300, 200], 1, 2, 64, 16)
+    for window, sinks in ((17, 0), (1, 0), (250, 3)):
+        s.check(s.run(window=window, sinks=sinks), window=window, sinks=sinks)
+
+
+def test_nan_in_one_of_many_parts():
+    s = Step(32, [40000], 1, 8, 1, 64, 64, garbage=False)
+    _, _, ks, vs = ref.offsets(64)
+    page, off = divmod(30001, 64)
+    row = s.cache[s.table[0, page], 0, off // 16]
+    keep = row[vs[off % 16, 1]]
+    row[vs[off % 16, 1]] = 255
+    got = s.run()
+    s.check(got)
+    assert np.isnan(got[0, :, 32:]).all() and not np.isnan(got[0, :, :32]).any()
+    row[vs[off % 16, 1]] = keep
+    row[ks[off % 16, 0]] = 255
+    assert np.isnan(s.run()[0]).all()
 
 
 def test_attention_value_scales_far_apart():
@@ -447,10 +518,10 @@ def test_slots_past_32_bits_of_bytes():
                      torch.tensor([0, 1], dtype=i32, device="cuda"),
                      torch.tensor([L], dtype=i32, device="cuda"), out)
     K, V = ref.decode(small)
-    o, avg, spread, floor = ref.attention(ref.bf16_to_f64(q), K, V, np.array([[1, 0]]), np.array([0, 1]),
+    o, avg, spread, total = ref.attention(ref.bf16_to_f64(q), K, V, np.array([[1, 0]]), np.array([0, 1]),
                                    np.array([L]), page, D ** -0.5)[0]
     err = np.abs(ref.bf16_to_f64(to_bits(out))[0] - o)
-    assert (err <= ref.attention_tolerance(o, avg, spread, floor, D)).all()
+    assert (err <= ref.attention_tolerance(o, avg, spread, total, D)).all()
 
 
 def test_streams_and_graphs():
@@ -548,8 +619,8 @@ def test_a_decode_run_into_the_layer_tail():
                 dst[r, :, :len(x)] = ref.values(*ref.quantize(np.stack(x, 1)))
         want = ref.attention(qn, K, V, np.arange(R)[:, None].repeat(Lm, 1), starts_h, kv_h, Lm, D ** -0.5)
         got = ref.bf16_to_f64(to_bits(out))
-        for i, (o, avg, spread, floor) in want.items():
-            assert (np.abs(got[i] - o) <= ref.attention_tolerance(o, avg, spread, floor, D)).all()
+        for i, (o, avg, spread, total) in want.items():
+            assert (np.abs(got[i] - o) <= ref.attention_tolerance(o, avg, spread, total, D)).all()
         lens.copy_(kv)
     assert int(st) == 0
     # the last step's rows through the layer tail
@@ -565,5 +636,89 @@ def test_a_decode_run_into_the_layer_tail():
     ids, _, _ = tail.routing(R)
     check_parity(to_bits(y), to_bits(res), ids, orc, shape.k,
                  residual_tol=bf16_step(x_orc) + bf16_step(orc["residual"]))
+    assert tail.status() == 0
+    tail.close()
+
+
+def test_a_captured_decode_step_follows_the_lengths():
+    """One graph of a whole step, replayed while the lengths in device memory grow: the same bits as
+    the calls one by one on a second cache."""
+    R, hq, heads, D, page, width = 3, 16, 2, 128, 16, 20
+    shape = gen.TailShape(R, 256, 8, 2, 128, 128, Ha=hq * D)
+    d = gen.make_weights(shape, 4, keys=gen._LAYER_WEIGHTS + ("w_o",))
+    tail = mt.MoeTail(shape, mt.weights_to_device(d), max_rows=R)
+    rng = np.random.default_rng(33)
+    i32 = torch.int32
+    freq = torch.from_numpy((10000.0 ** (-np.arange(0, D, 2) / D)).astype(np.float32)).cuda()
+    gain = to_dev(ref.f32_to_bf16(1 + 0.1 * rng.standard_normal(D).astype(np.float32)))
+    new = torch.ones(R, dtype=i32, device="cuda")
+    ws = torch.empty(mt.kv4_attention_workspace(hq, heads, D), dtype=torch.uint8, device="cuda")
+    first = torch.tensor([250, 15, 0], dtype=i32, device="cuda")
+
+    class Side:
+        def __init__(self):
+            self.cache = mt.kv4_cache(64, page, heads, D)
+            self.table = torch.full((R, width), -1, dtype=i32, device="cuda")
+            self.free = torch.arange(64, dtype=i32, device="cuda")
+            self.lens = first.clone()
+            self.qkv = torch.zeros((R, (hq + 2 * heads) * D), dtype=BF, device="cuda")
+            self.res = torch.zeros((R, 256), dtype=BF, device="cuda")
+            self.starts, self.kv = (torch.zeros(n, dtype=i32, device="cuda") for n in (R + 1, R))
+            self.pos, self.used = (torch.zeros(n, dtype=i32, device="cuda") for n in (R, 1))
+            self.slots = torch.zeros(R, dtype=torch.int64, device="cuda")
+            self.out = torch.zeros((R, hq, D), dtype=BF, device="cuda")
+            self.y = torch.zeros((R, 256), dtype=BF, device="cuda")
+            self.st = status_word()
+
+        def step(self):
+            q = self.qkv[:, :hq * D].view(R, hq, D)
+            k = self.qkv[:, hq * D:(hq + heads) * D].view(R, heads, D)
+            v = self.qkv[:, (hq + heads) * D:].view(R, heads, D)
+            mt.step_tables(self.lens, new, self.free, self.table, page, self.starts, self.kv, self.pos,
+                           self.slots, self.used, status=self.st)
+            mt.qk_norm_rope(q, k, gain, gain, self.pos, freq, q, k)
+            mt.kv4_append(self.cache, k, v, self.slots, status=self.st)
+            mt.kv4_attention(q, self.cache, self.table, self.starts, self.kv, self.out, workspace=ws,
+                             status=self.st)
+            tail.run_attn(self.out.view(R, hq * D), self.res, self.y)
+            self.lens.copy_(self.kv)
+
+    def prompts(side):  # the tokens that are there already
+        n = first.clone()
+        zero = torch.zeros_like(n)
+        T = int(n.sum())
+        pos, slots = torch.empty(T, dtype=i32, device="cuda"), torch.empty(T, dtype=torch.int64, device="cuda")
+        mt.step_tables(zero, n, side.free, side.table, page, side.starts, side.kv, pos, slots, side.used)
+        x = to_dev(normal_bits(np.random.default_rng(34), T, heads, D))
+        mt.kv4_append(side.cache, x, x, slots)
+        side.free = side.free[int(side.used):].clone()
+
+    one, two = Side(), Side()
+    prompts(one)
+    prompts(two)
+    one.step()  # (warm: what the calls set up once)
+    torch.cuda.synchronize()
+    fresh = Side()
+    prompts(fresh)
+    for name in ("cache", "table", "lens", "res", "free"):
+        getattr(one, name).copy_(getattr(fresh, name))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one.step()
+    torch.cuda.synchronize()
+    free = one.free.clone()
+    for step in range(8):
+        x = to_dev(normal_bits(rng, R, (hq + 2 * heads) * D))
+        for side in (one, two):
+            side.qkv.copy_(x)
+            side.free[:len(free)].copy_(free)
+        graph.replay()
+        two.step()
+        torch.cuda.synchronize()
+        for name in ("starts", "kv", "pos", "slots", "used", "table", "cache", "out", "res", "y", "lens"):
+            assert torch.equal(getattr(one, name), getattr(two, name)), (step, name)
+        assert int(one.st) == 0 and int(two.st) == 0
+        assert torch.equal(one.lens, first + step + 1)
+        free = torch.cat([free[int(one.used):], torch.full((int(one.used),), -1, dtype=i32, device="cuda")])
     assert tail.status() == 0
     tail.close()

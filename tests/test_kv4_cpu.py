@@ -100,7 +100,7 @@ def test_cache_rows_refuse(lib, fn, kw, code):
 
 ATTN = dict(rows=4, reqs=2, q_heads=16, kv_heads=2, head_dim=128, page_size=32, n_pages=4, q=A,
             ld_q=2048, cache=A, block_table=A, table_width=3, table_stride=3, row_starts=A, kv_lens=A,
-            scale=0.1, window=0, sinks=0, max_new=1, out=A, ld_o=2048, workspace=A,
+            scale=0.1, window=0, sinks=0, max_new=1, out=A + 4096, ld_o=2048, workspace=A,
             workspace_bytes=1 << 40, status=None, stream=None)
 
 
@@ -114,7 +114,7 @@ ATTN = dict(rows=4, reqs=2, q_heads=16, kv_heads=2, head_dim=128, page_size=32, 
     (dict(page_size=20), UNS), (dict(q=None), INV), (dict(q=A + 4), INV), (dict(cache=A + 8), INV),
     (dict(out=None), INV), (dict(workspace=None), INV), (dict(workspace=A + 8), INV),
     (dict(block_table=None), INV), (dict(row_starts=None), INV), (dict(kv_lens=None), INV),
-    (dict(ld_q=2040), INV), (dict(ld_o=2052), INV)])
+    (dict(ld_q=2040), INV), (dict(ld_o=2052), INV), (dict(out=A), INV)])
 def test_attention_refuses(lib, kw, code):
     assert _call(lib.moe_kv4_attention, ATTN, kw) == code
 
