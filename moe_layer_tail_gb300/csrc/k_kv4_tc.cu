@@ -106,7 +106,7 @@ struct Geo {
   // raw and operand rings, info ring, q, and the single ones
   static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 12 + 4;
   static constexpr int kSmall = kBars * 8 + kRaw * 20 * 4 /* t0, full */ + 4 * RN * 12 /* red, l */ +
-                                RN * 8 /* rowpos, nan */ + 64 + 32 /* over */;
+                                RN * 16 /* rowpos, nan */ + 64 + 32 /* over */;
   static constexpr size_t smem(int reqs) {
     return 1024 + (size_t)oSmall + kSmall + (size_t)(3 * reqs + 2) * 4;
   }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   using G = Geo<D, RN>;
   constexpr int NM = G::NM, NB = G::NB;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ uint64_t s_total;
+  __shared__ uint32_t s_range[3];  // of places: first, end, of each CTA
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead;
   uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 20);  // [2][4][RN]
   float* lsum = red + 8 * RN;                                       // [4][RN]
   int* rowpos = reinterpret_cast<int*>(lsum + 4 * RN);
-  uint32_t* nanrow = reinterpret_cast<uint32_t*>(rowpos + RN);
-  uint32_t* pre = nanrow + RN + 16;
+  uint32_t* nanrow = reinterpret_cast<uint32_t*>(rowpos + 2 * RN);  // both [2 turns][RN]
+  uint32_t* pre = nanrow + 2 * RN + 16;
   int* lens = reinterpret_cast<int*>(pre + a.reqs + 1);
   int* starts = lens + a.reqs;
 
@@ -349,7 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     const uint64_t total64 = plan(a, RN, plan_load(a, lane), pre, lens, starts, &bits);
     if (total64 > 0x7FFFFFFFull) bits |= kStatusBadLength;
     if (blockIdx.x == 0 && bits && a.status) atomicOr(a.status, bits);
-    if (lane == 0) s_total = total64 > 0x7FFFFFFFull ? 0 : total64;
+    const uint32_t total = total64 > 0x7FFFFFFFull ? 0u : (uint32_t)total64, per = range_tiles(total, a.ctas);
+    const uint32_t u0 = (uint32_t)min((uint64_t)blockIdx.x * per, (uint64_t)total);
+    __syncwarp();
+    const uint32_t u1 = range_end(a, RN, pre, lens, starts, u0, min(total, u0 + per));
+    if (lane == 0) s_range[0] = u0, s_range[1] = u1, s_range[2] = per;
   } else {
     // the identity (E2M1 code 2 is 1.0) in rows of 128 bytes, and its scales
     for (int i = tid < 64 ? tid : tid - 32; i < 128 * 8; i += kThreads - 32) {
@@ -366,10 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t total = (uint32_t)s_total, per = range_tiles(total, a.ctas);
-  const uint64_t u0w = (uint64_t)blockIdx.x * per;
+  const uint32_t u0 = s_range[0], u1 = s_range[1], per = s_range[2];
   const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
-  const uint32_t u0 = (uint32_t)min(u0w, (uint64_t)total), u1 = min(total, u0 + per);
   if (u0 == u1 && tid == 0) recs[blockIdx.x].last = -1;
 
   bool gone = false;  // a wait gave up, here or elsewhere in the CTA
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
             bulk_load(dst + (lane & 7) * G::kTile, a.cache + at, G::kTile, B.raw_full + st);
         }
       }
-      u += (uint32_t)(s.k1 - s.k0);
+      u += s.places;
     }
   } else if (warp == 1) {
     // --------------------------------------- the tensor cores: K' = K I, S^T = K' Q^T ----
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     for (uint32_t u = u0; u < u1; qr.next()) {
       const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
       r = s.r;
-      u += (uint32_t)(s.k1 - s.k0);
+      u += s.places;
       const int subs = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles * G::kHalves;
       const uint32_t q0 = base + G::oQ + qr.i * G::kQ;
       wait(B.q_full + qr.i, qr.ph);
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     for (uint32_t u = u0; u < u1;) {
       const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
       r = s.r;
-      u += (uint32_t)(s.k1 - s.k0);
+      u += s.places;
       const int subs = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles * G::kHalves;
       for (int st = 0; st < subs; ++st, ++n) {
         if (__any_sync(~0u, gone)) break;
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     const int quad = warp & 3;                       // tensor-memory lanes 32 quad ..
     const uint32_t tl = tm + ((uint32_t)quad << 21);  // (lane in bits 16..)
     const int tok = 32 * quad + lane;                // this thread's token of a step
-    uint8_t* over = reinterpret_cast<uint8_t*>(nanrow + RN) + half * 8;  // [2][4]: a warp's x passed kOver
+    uint8_t* over = reinterpret_cast<uint8_t*>(nanrow + 2 * RN) + half * 8;  // [2][4]: a warp's x passed kOver
     // where this token's numerators of rows k0 + k go (k and k + 8 lie 1024 bytes apart)
     uint8_t* ps[RH < 8 ? RH : 8];
 #pragma unroll
@@ -588,20 +590,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       ps[k] = sm + G::oP + quad * (NM * 128) + (k0 + k) * 128 + (((lane >> 2) ^ ((k0 + k) & 7)) << 4) + (lane & 3) * 4;
     float* hred = red + half * 4 * RH;  // [2 turns][2 halves][4][RH]
     float* hsum = lsum + half * 4 * RH;
-    int turn = 0;
-    uint32_t i = 0;
-    int r = r0;
-    for (uint32_t u = u0; u < u1;) {
-      const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
-      r = s.r;
-      const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first), row0 = starts[s.r];
-      const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
+    int turn = 0, part = 0;
+    uint32_t i = 0, checks = 0;
+    Seg s;
+    int first = 0, nrow = 0;
+    auto open = [&](int r, uint32_t u) {  // the part from u on, its rows' positions
+      s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+      first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first);
       if (quad == 0 && lane < RH) {
         const int k = k0 + lane;
-        rowpos[k] = k < nrow ? s.q.L - s.q.nq + (first + k) / a.G : INT32_MIN / 2;
-        nanrow[k] = 0;
+        rowpos[(part & 1) * RN + k] = s.q.L - s.q.nq + (first + min(k, nrow - 1)) / a.G;
+        nanrow[(part & 1) * RN + k] = 0;
       }
-      soft_sync(half);
+    };
+    if (u0 < u1) open(r0, u0);
+    soft_sync(half);
+    for (uint32_t u = u0; u < u1; ++part) {
+      const int* rowp = rowpos + (part & 1) * RN + k0;
+      uint32_t* nanr = nanrow + (part & 1) * RN + k0;
+      const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
       float l[RH], m[RH];
 #pragma unroll
       for (int k = 0; k < RH; ++k) l[k] = 0.f, m[k] = kLow;
@@ -622,26 +629,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           int t0 = inf.t0[tok >> 4], t = t0 < 0 ? INT32_MAX : t0 + (tok & 15);
           fl = inf.flags[tok];
           if (inf.plain >> (8 * (tok >> 4)) & 1) t = INT32_MIN, fl = 0;
-          seen = 0;
+          // the rows' positions ascend: most tokens are seen by all of them or by none
+          const int p0 = rowp[0], p1 = rowp[RH - 1];
+          const bool out = a.window != 0 && t >= a.sinks;  // (only a window shows it)
+          if (t == INT32_MIN || (t <= p0 && !(out && t <= p1 - a.window))) {
+          } else if (t > p1 || (out && p0 >= 0 && t <= p0 - a.window)) {
+            seen = 0;
+          } else {
+            seen = 0;
 #pragma unroll
-          for (int k = 0; k < RH; ++k) {
-            const int p = rowpos[k0 + k];
-            if (t == INT32_MIN || (t <= p && (a.window == 0 || t > p - a.window || t < a.sinks))) seen |= 1u << k;
-            if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);  // a NaN among the key scales
-            if (!(seen >> k & 1)) x[k] = -INFINITY;
-            if ((fl & 255u) && (seen >> k & 1)) atomicOr(nanrow + k0 + k, fl & 255u);  // value scales
+            for (int k = 0; k < RH; ++k) {
+              const int p = rowp[k];
+              if (t <= p && !(out && t <= p - a.window)) seen |= 1u << k;
+            }
+          }
+          if (__any_sync(~0u, fl != 0 || seen != ~0u)) {
+#pragma unroll
+            for (int k = 0; k < RH; ++k) {
+              if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);  // a NaN among the key scales
+              if (!(seen >> k & 1)) x[k] = -INFINITY;
+              else if (fl & 255u) atomicOr(nanr + k, fl & 255u);  // value scales
+            }
           }
         }
-        float top = -INFINITY;
+        bool move = st == 0;  // the rows' references move
+        const uint32_t cb = checks & 1;
+        if (!move) {
+          float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < RH; ++k) {
-          x[k] = fmaf(x[k], a.scale_log2, -m[k]);
-          top = fmaxf(top, x[k]);
-        }
-        const bool mine = __any_sync(~0u, top > kOver);
-        if (lane == 0) {
-          over[4 * b + quad] = mine;
-          mbar_arrive(B.soft + 2 * half + b);
+          for (int k = 0; k < RH; ++k) {
+            x[k] = fmaf(x[k], a.scale_log2, -m[k]);
+            top = fmaxf(top, x[k]);
+          }
+          const bool mine = __any_sync(~0u, top > kOver);
+          if (lane == 0) {
+            over[4 * cb + quad] = mine;
+            mbar_arrive(B.soft + 2 * half + cb);
+          }
         }
         if (!d1) wait(B.pv + b, (i >> 1) + 1);
         const uint32_t pb = b * G::kP;
@@ -653,19 +677,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
             *reinterpret_cast<float*>(ps[k & 7] + pb + (k >> 3) * 1024) = to_tf32(p[k]);
           }
         };
-        numerators();
-        wait(B.soft + 2 * half + b, i >> 1);
-        if (*reinterpret_cast<volatile uint32_t*>(over + 4 * b)) {
-          // the rows' references move to the maxima over this step's 128 tokens (from the scores
-          // themselves: against the initial reference x has lost them)
-          tmem_ld<RH>(sa, x);
+        if (!move) {
+          numerators();
+          wait(B.soft + 2 * half + cb, checks++ >> 1);
+          move = *reinterpret_cast<volatile uint32_t*>(over + 4 * cb) != 0;
+          if (move) {  // from the scores themselves
+            tmem_ld<RH>(sa, x);
+#pragma unroll
+            for (int k = 0; k < RH; ++k) {
+              if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);
+              if (!(seen >> k & 1)) x[k] = -INFINITY;
+            }
+          }
+        }
+        if (move) {
+          // to the maxima over this step's 128 tokens
           float y[RH];
 #pragma unroll
-          for (int k = 0; k < RH; ++k) {
-            if (fl >> 15) x[k] = __uint_as_float(0x7FC00000u);
-            x[k] = (seen >> k & 1) ? x[k] * a.scale_log2 : -INFINITY;
-            y[k] = x[k];
-          }
+          for (int k = 0; k < RH; ++k) y[k] = x[k] = x[k] * a.scale_log2;
           const float w = warp_max_of<RH>(y);
           float* hr = hred + (turn ^= 1) * 8 * RH;  // (the turn before may still be read)
           if (lane < RH) hr[quad * RH + lane] = w;
@@ -703,33 +732,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         if (lane == 0) mbar_arrive(B.p_full + b);
       }
 
-      // ---- the part's sums and averages
+      // ---- the part's sums and averages; what need not wait for the last product, the next part's
+      // opening among it, comes first
       const float lw = warp_sum_of<RH>(l);
       if (lane < RH) hsum[quad * RH + lane] = lw;
-      wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
-      fence_after();
-      soft_sync(half);
-      // the joining launch may line up now (from the start on, its CTAs had cost 2 us a call)
-      if (u + (uint32_t)(s.k1 - s.k0) >= u1) mtail::pdl_trigger();
       const bool whole = s.k0 == 0 && s.k1 == s.q.n;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (s.k0 == 0 ? 1 : 0);
-      // lane k of each warp: where row k0 + k goes, 1 / sum and its NaN blocks
+      const int rows = nrow;
+      // lane k of each warp: where row k0 + k goes
       const int kl = k0 + (lane < RH ? lane : 0);
-      const float sum = (hsum[kl - k0] + hsum[RH + kl - k0]) + (hsum[2 * RH + kl - k0] + hsum[3 * RH + kl - k0]);
-      const float inv_l = sum == 0.f ? 0.f : 1.f / sum;
-      const uint32_t nan_l = nanrow[kl];
-      int64_t at_l;
+      int64_t at_l = (slot * RN + kl) * D;
       if (whole) {
         const int rho = first + kl, tk = rho / a.G;
-        at_l = (row0 + tk) * a.ldo + (int64_t)(s.h * a.G + rho - tk * a.G) * D;
+        at_l = (starts[s.r] + tk) * a.ldo + (int64_t)(s.h * a.G + rho - tk * a.G) * D;
+      }
+      u += s.places;
+      if (u >= u1) {
+        if (warp == 4 && lane == 0) {
+          JoinRec rec;
+          rec.last = s.k0 == 0 && !whole ? (int)((s.item + (uint32_t)(s.q.n + kItemTiles) - 1) / per) : -1;
+          rec.row0 = starts[s.r], rec.first = first, rec.head = s.h, rec.rows = nrow;
+          rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
+          recs[blockIdx.x] = rec;
+        }
       } else {
-        at_l = (slot * RN + kl) * D;
+        ++part;
+        open(s.r, u);
+        --part;
+      }
+      soft_sync(half);
+      // ... its 1 / sum and its NaN blocks
+      const float sum = (hsum[kl - k0] + hsum[RH + kl - k0]) + (hsum[2 * RH + kl - k0] + hsum[3 * RH + kl - k0]);
+      const float inv_l = sum == 0.f ? 0.f : 1.f / sum;
+      const uint32_t nan_l = nanr[kl - k0];
+      const bool nans = __any_sync(~0u, nan_l != 0);
+      if (!whole) {
         float* pml = a.part + 2 * (int64_t)a.ctas * RN * D + slot * RN * 2;
         float mk = m[0];
 #pragma unroll
         for (int k = 1; k < RH; ++k) mk = lane == k ? m[k] : mk;
-        if (quad == 0 && lane < RH && kl < nrow) *reinterpret_cast<float2*>(pml + 2 * kl) = make_float2(mk, sum);
+        if (quad == 0 && lane < RH && kl < rows) *reinterpret_cast<float2*>(pml + 2 * kl) = make_float2(mk, sum);
       }
+      wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
+      fence_after();
+      // the joining launch may line up now (from the start on, its CTAs had cost 2 us a call)
+      if (u >= u1) mtail::pdl_trigger();
 #pragma unroll
       for (int h = 0; h < G::kHalves; ++h) {
         float o[RH];
@@ -739,23 +786,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         for (int k = 0; k < RH; ++k) {
           const int64_t at = __shfl_sync(~0u, at_l, k);
           float v = o[k] * __shfl_sync(~0u, inv_l, k);
-          if (__shfl_sync(~0u, nan_l, k) >> (ch >> 5) & 1) v = __uint_as_float(0x7FC00000u);
-          if (k0 + k < nrow && tok < G::CH) {
+          if (nans && (__shfl_sync(~0u, nan_l, k) >> (ch >> 5) & 1)) v = __uint_as_float(0x7FC00000u);
+          if (k0 + k < rows && tok < G::CH) {
             if (whole) a.out[at + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             else a.part[at + ch] = v;
           }
         }
       }
-      u += (uint32_t)(s.k1 - s.k0);
-      if (u >= u1 && warp == 4 && lane == 0) {
-        JoinRec rec;
-        rec.last = s.k0 == 0 && !whole ? (int)((s.item + (uint32_t)s.q.n - 1) / per) : -1;
-        rec.row0 = row0, rec.first = first, rec.head = s.h, rec.rows = nrow;
-        rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
-        recs[blockIdx.x] = rec;
-      }
       fence_before();
-      soft_sync(half);  // (the next part's notes overwrite these)
     }
   } else {
     // ----------------------------------------- cached bytes into the tensor cores' operands ----
@@ -902,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           mbar_arrive(B.op_full + op.i);
         }
       }
-      u += (uint32_t)(s.k1 - s.k0);
+      u += s.places;
     }
   }
 
