@@ -456,10 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       const uint32_t h = n % G::kHalves;
       const uint32_t ob = base + G::oOp + op.i * G::kOp, sb = base + G::oSf + op.i * G::kSf;
       const uint32_t sf = tm + G::cSfK + (n / G::kHalves & 1) * 4 * G::kAtoms;
-      if (h == 0) wait(B.op_full + op.i, op.ph);
-      if (n > 0) {  // the scores of the sub-step before: the keys are used up
-        if (G::kHalves > 1) wait(B.k_free, n - 1);
-        else wait(B.s_full + ((n - 1) & 1), (n - 1) >> 1);
+      // the operands, and the scores of the sub-step before: the keys are used up
+      if (G::kHalves > 1) {
+        if (h == 0) wait(B.op_full + op.i, op.ph);
+        wait(B.k_free, n + 1);
+      } else if (n > 0) {
+        wait2(B.op_full + op.i, op.ph, B.s_full + ((n - 1) & 1), (n - 1) >> 1);
+      } else {
+        wait(B.op_full + op.i, op.ph);
       }
       fence_after();
       if (elect_one()) {
@@ -553,8 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       for (int st = 0; st < subs; ++st, ++n) {
         if (__any_sync(~0u, gone)) break;
         const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1, nb = n & 1;
+        // (with two halves the next values would come too late behind this product, with one this
+        // product behind the next values)
         bool next = st + 1 < subs || u < u1;
-        if (next && __all_sync(~0u, mbar_test(B.op_full + op.i, op.ph))) {
+        if (G::kHalves > 1 && next && __all_sync(~0u, mbar_test(B.op_full + op.i, op.ph))) {
           v_ident(n + 1);
           next = false;
         }
