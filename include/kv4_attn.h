@@ -139,12 +139,12 @@ int moe_kv4_read(int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t page_
  * and does not change what is computed.  `workspace` (16-byte aligned, exclusive to the call
  * until it has completed) holds workspace_bytes >= moe_kv4_attention_workspace(..) with the same
  * arguments on this device.
- * Arithmetic: q is taken as f16 scaled by a power of two for each row (exact for values within
- * 2^28 of the row's largest), products with the E2M1 codes are exact, sums, scales, softmax
- * statistics and the output sums are fp32; the softmax numerators enter the second product as f16
- * times the value scale.  The split of the work depends on the lengths of all requests and on
- * the device, so the same request in another batch may differ in the last bits; the same call
- * always gives the same bits.
+ * Arithmetic: queries and cached keys enter the scores exactly (tf32 holds both), scores, scale,
+ * softmax statistics and output sums are fp32; the softmax numerators are rounded to tf32 for the
+ * product with the exact values, the sum that divides takes them unrounded.  A numerator may reach
+ * 2^40 (the reference is not always the maximum), so sums of values past 2^60 or so may overflow.
+ * The split of the work depends on the lengths of all requests and on the device, so the same
+ * request in another batch may differ in the last bits; the same call always gives the same bits.
  * rows 1..2^20, reqs 1..1024, kv_heads 1..256, q_heads a multiple of it with q_heads / kv_heads
  * <= 256, D in {64, 128, 256}, page_size a multiple of 16 up to 1024, n_pages 1..2^31-1,
  * scale finite and > 0, window >= 0, sinks >= 0 (ignored when window == 0), max_new >= 1; q, out,

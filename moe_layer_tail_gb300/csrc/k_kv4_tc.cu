@@ -6,9 +6,10 @@
 // in one pass over the cache.  The query heads that share a kv head, and the rows of a request,
 // are rows of one work item (RN at a time), so the cache is read once for all of them; the items'
 // tiles of 16 tokens, laid end to end, are cut into equal ranges, one per SM (k_kv4_plan.cuh), so
-// that ragged lengths, one long request and many short ones all load every SM the same.  An item
-// that lies in one range is written by its CTA; the others leave an average and (max, sum) per row
-// and part in the workspace, which a second launch joins (programmatic dependent launch).
+// that ragged lengths, one long request and many short ones all load every SM the same (32 requests
+// of up to 32768 tokens run at the rate of one of 524287).  An item that lies in one range is
+// written by its CTA; the others leave an average and (max, sum) per row and part in the workspace,
+// which a second launch joins (programmatic dependent launch).
 //
 // The CUDA cores never see a key or a value.  A step is 8 tiles (128 tokens) of one kv head:
 //   K' [128 tokens x D] = K I      tcgen05 kind::mxf4 block-scaled, the codes and scales as they
@@ -16,22 +17,42 @@
 //                                  fp32, in tensor memory;
 //   S^T [128 x RN] = K' Q^T        kind::tf32, K' read from tensor memory as operand A, the bf16
 //                                  queries exact as tf32 in shared memory;
-//   P^T = 2^(S - m)                fp32 on the CUDA cores, a token per thread, rounded to tf32 (the
-//                                  row's sum adds the rounded numerators, so the rounding has no
-//                                  bias); m is the maximum over the item's first step and moves
-//                                  again only when a score passes it by 40 octaves;
+//   P^T = 2^(S - m)                fp32 on the CUDA cores, a token per thread, rounded to tf32 for
+//                                  the product (half a step, 2^-11 of each term: the least that a
+//                                  tensor-core operand of this range costs; the row's sum takes them
+//                                  unrounded); m is the row's maximum over the part's first step
+//                                  and moves only when a score passes it by 40 octaves, since a
+//                                  move rescales O and holds the products up;
 //   V' [D x 128 tokens] = I V^T    the dequantised values, transposed by the product itself;
 //   O^T [D x RN] += V' P^T         kind::tf32, V' from tensor memory, accumulating there.
-// On a GB300 the products of one step (D 128, RN 16) take 2 x 126 + 2 x 150 of the 740 cycles in
-// which its 17 KB arrive at the measured copy rate; conversions on the CUDA cores into mma.sync
-// had taken 490 warp instructions per tile and stayed at 2.5 TB/s.
+// Conversions on the CUDA cores into mma.sync had taken 490 warp instructions per tile and stayed
+// at 2.5 TB/s.
+//
+// What bounds it (524287 tokens, 8 kv heads of 128, 16 query heads each: 570 MB in 135 us, 4.2 TB/s,
+// 0.62 of the measured copy rate): not the tensor cores (about 550 cycles of products a step), not
+// the memory (740 cycles for a step's 17 KB) but two chains of hand-overs of about 1100 cycles a
+// step each, K' -> S -> K' of the next step (each product is seen complete about 300 cycles after
+// its last instruction has issued, and K' has room for one step only) and S -> P -> S of the
+// softmax.  Tensor memory is full at D 128 (K' 128 columns, V' 2 x 128, S, O, scales of 512), so
+// neither can run further ahead.  Tried and slower at this size: K' in a ring of three blocks of 64
+// channels with a warp of its own (163 us: six runs of products a step instead of four, and each
+// costs the pipe some 150 cycles beside its products); both dequantisations in one run (160); V'
+// and K' in halves (234); waits that poll (185; a dozen polling warps take the shared-memory pipe
+// from the others); one group of four softmax warps (190).  D 64 has the same chains for half the
+// bytes; D 256 twice the products for its two halves of channels.
 //
 // Warps: 0 looks up pages and copies tiles (bulk copies into a ring, 32 look-ups at a time);
 // 6..13 (one per tile of a step) bring a tile's bytes, which the cache holds in the order of
 // register fragments, into the swizzled rows and scale-factor atoms of the tensor cores' operands;
-// 1 issues the products (one elected thread: a divergent issuer costs 45 cycles an instruction, an
-// elected one 9 at these sizes); 2..5 are the softmax and the output.  They hand over through
-// mbarriers; every wait is bounded and reports MOE_TAIL_STATUS_TIMEOUT.
+// 1 issues K' and S, 14 V' and O (an elected thread each: a divergent issuer costs 45 cycles an
+// instruction, an elected one 9 at these sizes); 2..5 and 15..18 are the softmax and the output of
+// the lower and the upper half of the rows.  They hand over through mbarriers; every wait is bounded
+// and reports MOE_TAIL_STATUS_TIMEOUT.  Spills must stay out of the steps: local memory shares what
+// little L1 the 150..210 KB of shared memory leave, and versions that spilled took 2.5 times as long.
+//
+// Tensor memory is taken whole (512 columns) before the previous kernel in the stream has ended.
+// That cannot lock up: no other tensor-memory kernel of this library fits beside a CTA of this one
+// (shared memory), and this one's CTAs hold theirs before they let the next kernel line up.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
