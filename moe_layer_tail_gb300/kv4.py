@@ -275,19 +275,28 @@ def kv4_attention(q, cache, block_table, row_starts, kv_lens, out, scale: float 
     prs = _flat(w, "row_starts", row_starts, i32, dev, reqs + 1)
     pkl = _flat(w, "kv_lens", kv_lens, i32, dev, reqs)
     st = None if status is None else _flat(w, "status", status, i32, dev, 1)
-    if workspace is None:
-        key = (dev, hq, heads, D, max_new)
-        n = _workspace_bytes.get(key)
-        if n is None:
-            n = _workspace_bytes[key] = kv4_attention_workspace(hq, heads, D, max_new, dev)
-        if stream is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        else:  # memory of the launching stream: the allocator reuses it only behind this call
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    n = workspace.numel()
-    pw = _flat(w, "workspace", workspace, torch.uint8, dev, n)
     sc = D ** -0.5 if scale is None else scale
-    _launch(w, torch, dev, stream, lambda s: lib.moe_kv4_attention(
-        T, reqs, hq, heads, D, page, n_pages, pq, ldq, pc, pt, width, ld, prs, pkl, sc, window, sinks,
-        max_new, po, ldo, pw, n, st, s))
+    if workspace is not None:
+        n = workspace.numel()
+        pw = _flat(w, "workspace", workspace, torch.uint8, dev, n)
+        _launch(w, torch, dev, stream, lambda s: lib.moe_kv4_attention(
+            T, reqs, hq, heads, D, page, n_pages, pq, ldq, pc, pt, width, ld, prs, pkl, sc, window,
+            sinks, max_new, po, ldo, pw, n, st, s))
+        return
+    key = (dev, hq, heads, D, max_new)
+    n = _workspace_bytes.get(key)
+    if n is None:
+        n = _workspace_bytes[key] = kv4_attention_workspace(hq, heads, D, max_new, dev)
+
+    def call(s):
+        # memory of the launching stream: the allocator reuses it only behind this call (a tensor
+        # would do, for 5 us more on the host)
+        p = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, s)
+        try:
+            return lib.moe_kv4_attention(
+                T, reqs, hq, heads, D, page, n_pages, pq, ldq, pc, pt, width, ld, prs, pkl, sc, window,
+                sinks, max_new, po, ldo, p, n, st, s)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(p)
+
+    _launch(w, torch, dev, stream, call)

@@ -563,6 +563,35 @@ def test_streams_and_graphs():
         assert np.array_equal(ref.bf16_to_f64(to_bits(o))[:T], plain[:T])
 
 
+def test_a_captured_call_keeps_the_workspace_it_took():
+    # without a workspace argument the memory belongs to the graph: calls and tensors that come
+    # between capture and replay, in this stream and in others, do not share it
+    s = Step(35, [3000, 1333], 1, 8, 2, 128, 16)
+    plain = s.run()
+    i32 = torch.int32
+    q = to_dev(s.q)
+    cache = torch.from_numpy(s.cache).cuda()
+    table, starts, lens = (torch.tensor(x, dtype=i32, device="cuda") for x in (s.table, s.starts, s.lens))
+    outs = [torch.full_like(q, 5.0) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        mt.kv4_attention(q, cache, table, starts, lens, outs[0])
+    n = mt.kv4_attention_workspace(16, 2, 128)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        graph.replay()
+        mt.kv4_attention(q, cache, table, starts, lens, outs[1], stream=other)
+        with torch.cuda.stream(other):
+            junk = torch.full((n // 4,), float("nan"), device="cuda")
+            mt.kv4_attention(q, cache, table, starts, lens, outs[2])
+            del junk
+    torch.cuda.synchronize()
+    for o in outs:
+        assert np.array_equal(ref.bf16_to_f64(to_bits(o))[:2], plain[:2])
+
+
 def test_a_decode_run_into_the_layer_tail():
     """Steps of four requests as a server runs them: tables from the lengths, norm and rotation,
     cache rows, attention, then the layer tail with its output projection."""
