@@ -58,6 +58,7 @@ struct RowsArgs {
   int rows, heads, D, page;
   int64_t n_slots;      // n_pages * page
   uint64_t page_magic;  // ceil(2^64 / page): slot / page by a multiply
+  uint64_t head_magic;  // ceil(2^64 / heads) (of two heads and more)
   uint8_t* cache;
   uint16_t* k;  // read by the append, written by the read
   uint16_t* v;

@@ -35,6 +35,26 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
 }
+// two floats side by side: one instruction for both
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | (uint64_t)__float_as_uint(hi) << 32;
+}
+__device__ __forceinline__ float lower(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float upper(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ void unpack8(const uint4& u, uint64_t (&f)[4]) {
+  f[0] = pair(bf16_lo(u.x), bf16_hi(u.x)), f[1] = pair(bf16_lo(u.y), bf16_hi(u.y));
+  f[2] = pair(bf16_lo(u.z), bf16_hi(u.z)), f[3] = pair(bf16_lo(u.w), bf16_hi(u.w));
+}
 int num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -222,16 +242,19 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
     ug = *(reinterpret_cast<const uint4*>(gain) + li);
     ugo = *(reinterpret_cast<const uint4*>(gain) + other);
   }
-  uint4(*ring)[32] = s_ring[warp];
-  auto fetch = [&](int v) {  // (a group of copies for each v, empty behind the last)
-    const int i = v * G + gi;
-    if (i < n && act) cp_async16(&ring[v % kDepth][lane], in + i * a.D);
+  uint4* const ring = &s_ring[warp][0][lane];
+  const uint16_t* next = in + gi * a.D;  // of this lane group's next head
+  const int step_d = G * a.D, left0 = act ? (n - gi + G - 1) / G : 0;  // its heads
+  int ahead = 0;
+  auto fetch = [&]() {  // (a group of copies each time, empty behind the last)
+    if (ahead < left0) cp_async16(ring + (ahead % kDepth) * 32, next);
     asm volatile("cp.async.commit_group;" ::: "memory");
+    ++ahead, next += step_d;
   };
 #pragma unroll
-  for (int v = 0; v < kDepth; ++v) fetch(v);
+  for (int v = 0; v < kDepth; ++v) fetch();
 
-  float c[8], s[8];  // cos', sin'
+  uint64_t c[4], s[4];  // cos', sin'
   {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -243,47 +266,57 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
     unpack8(ugo, go);
     if (blocks) __syncthreads();
     else __syncwarp();
+    float cf[8], sf[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      c[e] = g[e], s[e] = 0.f;
+      cf[e] = g[e], sf[e] = 0.f;
       if (turns) {
         const int f = a.interleaved ? 4 * li + e / 2 : 8 * (low ? li : other) + e;
         const bool front = a.interleaved ? e % 2 == 0 : low;
-        c[e] = g[e] * cosines[f];
-        s[e] = (a.interleaved ? g[e ^ 1] : go[e]) * (front ? -sines[f] : sines[f]);
+        cf[e] = g[e] * cosines[f];
+        sf[e] = (a.interleaved ? g[e ^ 1] : go[e]) * (front ? -sines[f] : sines[f]);
       }
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = pair(cf[2 * e], cf[2 * e + 1]), s[e] = pair(sf[2 * e], sf[2 * e + 1]);
   }
-  for (int v = 0; v * G < n; ++v) {  // (uniform over the warp)
-    const int i = v * G + gi;
+  uint16_t* to = out + gi * a.D;
+  const int partner = other - li;
+  for (int v = 0; v * G < n; ++v, to += step_d) {  // (uniform over the warp)
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
     __syncwarp();
-    const uint4 u = act && i < n ? ring[v % kDepth][lane] : make_uint4(0, 0, 0, 0);
-    float x[8], y[8];
+    const uint4* at = ring + (v % kDepth) * 32;
+    const uint4 u = v < left0 ? *at : make_uint4(0, 0, 0, 0);
+    uint64_t x[4], y[4];
     unpack8(u, x);
     if (a.interleaved) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+      for (int e = 0; e < 4; ++e) y[e] = pair(upper(x[e]), lower(x[e]));
     } else {
-      unpack8(ring[v % kDepth][gi * L + other], y);  // (used where it turns)
+      unpack8(at[partner], y);  // (used where it turns)
     }
     __syncwarp();
-    fetch(v + kDepth);
+    fetch();
     float rs = 1.f;
     if (gain) {
-      float ss = 0.f;
+      uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
+      float ss = lower(s2) + upper(s2);
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
       rs = rsqrtf(fmaf(ss, inv_d, a.eps));
     }
+    const uint64_t rs2 = pair(rs, rs);
+    uint32_t r[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = x[e] * rs * c[e];
-      if (turns) x[e] = fmaf(y[e] * rs, s[e], x[e]);  // (else nothing of the partner: it may be infinite)
+    for (int e = 0; e < 4; ++e) {
+      uint64_t t = mul2(x[e], c[e]);
+      if (turns) t = fma2(y[e], s[e], t);  // (else nothing of the partner: it may be infinite)
+      t = mul2(t, rs2);
+      r[e] = pack2(lower(t), upper(t));
     }
-    if (i < n && act) *reinterpret_cast<uint4*>(out + i * a.D) = pack8(x);
+    if (v < left0) *reinterpret_cast<uint4*>(to) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -303,6 +336,9 @@ __device__ __forceinline__ uint8_t* tile_of(const RowsArgs& a, int64_t slot, int
   const int off = (int)(slot - page * a.page);
   return a.cache + ((page * a.heads + h) * (a.page / 16) + off / 16) * (17 * D);
 }
+__device__ __forceinline__ uint32_t row_of(const RowsArgs& a, uint32_t id) {  // id / heads
+  return a.heads == 1 ? id : (uint32_t)__umul64hi(id, a.head_magic);
+}
 // byte n of lane l of a tile's codes
 __device__ __forceinline__ int lane_byte(int n, int l) { return (n >> 4) * 512 + l * 16 + (n & 15); }
 
@@ -310,10 +346,11 @@ __device__ __forceinline__ int lane_byte(int n, int l) { return (n >> 4) * 512 +
 __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t* scale) {
   // the block's largest magnitude as bf16 bits: an infinity or a NaN (exponent 255) is larger
   // than every number
-  uint32_t am = max(max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu), max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu));
-  am = max(am, max(max(u.z & 0x7FFFu, (u.z >> 16) & 0x7FFFu), max(u.w & 0x7FFFu, (u.w >> 16) & 0x7FFFu)));
-  am = max(am, __shfl_xor_sync(~0u, am, 1));
-  am = max(am, __shfl_xor_sync(~0u, am, 2));
+  const uint32_t mask = 0x7FFF7FFFu;
+  const uint32_t a2 = __vmaxu2(__vmaxu2(u.x & mask, u.y & mask), __vmaxu2(u.z & mask, u.w & mask));
+  uint32_t am = __vmaxu2(a2, __shfl_xor_sync(~0u, a2, 1));
+  am = __vmaxu2(am, __shfl_xor_sync(~0u, am, 2));
+  am = max(am & 0xFFFFu, am >> 16);
   if (am >= 0x7F80u) {
     *scale = 255;
     return 0;
@@ -322,10 +359,14 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t* scale) {
   const int e = min(max((int)(am >> 7) - 129 + ((am & 0x7Fu) > 0x40u ? 1 : 0), -126), 125);
   *scale = (uint32_t)(e + 127);
   const float inv = mtail::exp2_int(-e);
+  uint64_t x2[4];
+  unpack8(u, x2);
   float x[8];
-  unpack8(u, x);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] *= inv;
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t t = mul2(x2[j], pair(inv, inv));
+    x[2 * j] = lower(t), x[2 * j + 1] = upper(t);
+  }
   return mtail::e2m1x8_pack(x);
 }
 
@@ -342,7 +383,7 @@ __global__ void __launch_bounds__(256) k_kv4_append(const RowsArgs a) {
   uint4 ku[kPairs], vu[kPairs];
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) {
-    const uint32_t id = id0 + p * (256 / L), row = id / (uint32_t)a.heads;
+    const uint32_t id = id0 + p * (256 / L), row = row_of(a, id);
     h[p] = id - row * (uint32_t)a.heads;
     slot[p] = -1;
     ku[p] = vu[p] = make_uint4(0, 0, 0, 0);
@@ -417,7 +458,7 @@ __global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) {
     const uint32_t id = id0 + p * (256 / L);
-    row[p] = id / (uint32_t)a.heads, h[p] = id - row[p] * (uint32_t)a.heads;
+    row[p] = row_of(a, id), h[p] = id - row[p] * (uint32_t)a.heads;
     slot[p] = row[p] < (uint32_t)a.rows ? a.slots[row[p]] : -1;
   }
 #pragma unroll
