@@ -179,9 +179,11 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
 // y the scaled channel, y' its partner, cos' = gain cos, sin' = partner's gain times +-sin.  The
 // heads come through a ring in shared memory, kDepth asynchronous copies of 512 bytes ahead of
 // their use and the first of them while the angles are formed: in registers as many would leave
-// room for half the warps (kMore = 3 of them: 68 us, the ring 61).  8192 rows of 64 + 8 heads of 128
-// take 61 us (302 MB, 4.95 TB/s, 0.73 of the measured copy rate), bounded by the instructions of the
-// norm and rotation beside the loads; one row takes 2.6 us, 32 rows of D 256 2.9: launches.
+// room for half the warps (three of them: 68 us, the ring 59).  8192 rows of 64 + 8 heads of 128 take
+// 59 us (302 MB, 5.1 TB/s, 0.75 of the measured copy rate), bounded by the instructions (issue slots
+// 77 % busy with single floats, before pairs of them were taken together); CTAs of one row each,
+// which form its angles together, take 69 there, but are what serves a few rows (2.6 us for one row,
+// 2.9 for 32 of D 256: launches).
 //
 // Angles: positions reach 2^31, where a product in 32 bits has lost the fraction of a turn and one
 // in fp64 is slow on this part.  So the frequency is taken in turns as a 64-bit binary fraction,
@@ -324,8 +326,9 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
 //
 // D/8 lanes hold one token's head, eight channels each, of its keys and of its values, so that a
 // block of 32 channels is four neighbouring lanes: its largest magnitude is two shuffles, and a
-// lane's eight codes are one word.  65537 rows of 8 heads of 128: in 75 us (4.5 TB/s over 340 MB, 0.67
-// of the measured copy rate), out 61 us (5.5 TB/s, 0.81); 32 rows in and out 3.6 us, two launches.  A
+// lane's eight codes are one word.  65537 rows of 8 heads of 128: in 68 us (5.0 TB/s over 340 MB, 0.73
+// of the measured copy rate; the instructions bound it, issue slots were 78 % busy at 75 us), out 61
+// us (5.5 TB/s, 0.82); 32 rows in and out 3.4 us, two launches.  A
 // token's bytes lie in 8- and 1-byte pieces all over its tile, so partial sectors reach the L2; tiles
 // put together in shared memory first took 103 us, as the two more barriers cost more than the sectors.
 
@@ -500,7 +503,7 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
   const int L = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, G = 32 / L;
   // One head per lane group and warp until every SM has 48 warps, then up to 16, in equal parts: the
   // angles are formed once per warp, and a ring is better used by a longer run (8192 rows of 64 + 8
-  // heads: 60 us with 16, 65 with 8).
+  // heads: 60 us with 16, 65 with 8, before the pairs of floats).
   const int64_t groups = (int64_t)a.rows * ((a.hq + a.hk + G - 1) / G), fill = (int64_t)num_sms() * 48;
   const int most = G * (int)std::min<int64_t>(std::max<int64_t>(groups / fill, 1), 16);
   auto split = [&](int heads, int& parts) {
@@ -531,7 +534,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
 template <bool kAppend>
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
   // One pair a group of lanes until the GPU is filled several times over (32 rows of 8 heads, in and
-  // out: 3.6 us, with two 4.5), then two (65537 rows: 134 us, with one 144).
+  // out: 3.6 us, with two 4.5), then two (65537 rows: 127 us).
   const int64_t threads = (int64_t)a.rows * a.heads * (a.D / 8);
   return threads < (int64_t)num_sms() * 2048 * 4 ? launch_rows<kAppend, 1>(a, st) : launch_rows<kAppend, 2>(a, st);
 }
