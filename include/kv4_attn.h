@@ -26,7 +26,8 @@
  * 2^125 with max |x| <= 6 * 2^(s-127), codes rounded to nearest, ties to even (magnitudes past
  * 6 * 2^125 saturate there: the next code would stand for 2^128); a block of 32 with an infinity
  * or a NaN gets the scale byte 255, which stands for NaN (its codes are 0).  The scale byte 0 is
- * read as 0 (nothing writes it but the caller's memset: a zeroed cache holds zeros).
+ * read as 0 (nothing writes it but the caller's memset: a zeroed cache holds zeros); 253 and 254
+ * are not part of the format.
  * One tile of 16 tokens (t = 0..15, channel d = 0..D-1) of one head is 17 * D bytes: 8 D bytes of
  * key codes, 8 D of value codes, D/2 key scale bytes, D/2 value scale bytes, each in the order in
  * which the lanes (g, c), g = 0..7, c = 0..3, of the matrix instructions read them:

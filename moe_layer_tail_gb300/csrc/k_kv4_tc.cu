@@ -983,7 +983,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
 // Joins the parts of the items that several ranges share.  CTA (x, y): the item that crosses the
 // end of range x for the first time, rows 4 y .. 4 y + 3, one per warp:
 //   out = sum_k w_k o_k / sum_k w_k,  w_k = l_k 2^(m_k - max m), in range order.
-// The first parts are on their way while the weights are formed.
+// The first parts are on their way while the weights are formed.  It reads its parts once (5 MB with
+// 16 rows of 128 in 152 ranges) and costs a call about 3 us, most of it a chain of three dependent
+// loads behind the main launch's end.
 template <int D, int RN>
 __global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ AttnArgs a) {
   extern __shared__ float sw[];  // [4][ctas]: weights of a warp's row

@@ -343,6 +343,23 @@ def test_attention_many_rows(D, G, new):
     s.check(s.run())
 
 
+@pytest.mark.parametrize("D,G,heads,new,lens", [
+    (64, 256, 1, 1, [70, 3]), (128, 1, 256, 1, [40]), (256, 1, 100, 1, [33, 1]), (64, 2, 255, 1, [18]),
+    (128, 4, 1, 513, [513]), (64, 1, 2, 400, [400, 1100])])
+def test_attention_at_the_limits_of_heads_and_rows(D, G, heads, new, lens):
+    s = Step(40, lens, new, G, heads, D, 16)
+    s.check(s.run())
+    s.check(s.run(max_new=1))  # an estimate that is off changes the cut, not what is computed
+
+
+def test_rows_before_the_first_request_and_wide_strides():
+    s = Step(41, [50, 20, 35], [2, 0, 1], 8, 2, 64, 16, pad=3)
+    s.starts = s.starts + 2  # two rows and the last one belong to nobody
+    got = s.run(stride=2048)
+    s.check(got)
+    assert (got[:2] == 5).all() and (got[5:] == 5).all()
+
+
 def test_attention_ragged_rows_and_empty_requests():
     s = Step(5, [5, 100, 3, 0, 257, 64], [2, 0, 3, 0, 1, 5], 8, 2, 128, 16)
     s.check(s.run(max_new=1))
