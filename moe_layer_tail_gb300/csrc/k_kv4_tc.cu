@@ -115,8 +115,9 @@ struct Geo {
   static constexpr int kAtoms = D == 256 ? 2 : 1;
   static constexpr int kSf = 2 * kAtoms * 512;           // key atoms, then value atoms
   static constexpr int kP = NM * 512, kQ = NM * D * 4;
-  // tensor-memory columns
-  static constexpr int cK = 0, cV = 128, cS = 384, cO = cS + 2 * NM;  // (K' once, V' twice)
+  // tensor-memory columns: K' once, V' twice (32 rows of D 256 leave room for one), S twice, O
+  static constexpr int kVs = D == 256 && RN == 32 ? 1 : 2;
+  static constexpr int cK = 0, cV = 128, cS = cV + 128 * kVs, cO = cS + 2 * NM;
   static constexpr int cSfK = cO + kHalves * NM, cSfV = cSfK + 8 * kAtoms, cSfI = cSfV + 8 * kAtoms, cSfJ = cSfI + 4;
   static_assert(cSfJ + 4 <= 512, "tensor memory");
   // shared memory (from a 1024-byte boundary)
@@ -131,6 +132,7 @@ struct Geo {
   static constexpr size_t smem(int reqs) {
     return 1024 + (size_t)oSmall + kSmall + (size_t)(3 * reqs + 2) * 4;
   }
+  static constexpr int kReqs = D == 256 && RN == 32 ? 256 : kMaxReqs;  // that it has room for
 };
 
 // ------------------------------------------------------------------ PTX wrappers ----
@@ -544,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     __syncwarp();
     Ring<G::kOps> op;  // of the values asked for next
     auto v_ident = [&](uint32_t n) {
-      const uint32_t h = n % G::kHalves, nb = n & 1;
+      const uint32_t h = n % G::kHalves, nb = n % G::kVs;
       const uint32_t ob = base + G::oOp + op.i * G::kOp, sb = base + G::oSf + op.i * G::kSf + 512 * G::kAtoms;
       const uint32_t sf = tm + G::cSfV + (n / G::kHalves & 1) * 4 * G::kAtoms;
-      // the operands, and the product two sub-steps ago that read the values in this place
-      wait2(B.op_full + op.i, op.ph, (G::kHalves > 1 ? B.v_free : B.pv) + nb, (n >> 1) + 1);
+      // the operands, and the last product that read the values in this place
+      wait2(B.op_full + op.i, op.ph, (G::kHalves > 1 ? B.v_free : B.pv) + nb, n / G::kVs + 1);
       fence_after();
       if (elect_one()) {
         if (h == 0) {
@@ -577,15 +579,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       const int subs = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles * G::kHalves;
       for (int st = 0; st < subs; ++st, ++n) {
         if (__any_sync(~0u, gone)) break;
-        const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1, nb = n & 1;
+        const uint32_t i = n / G::kHalves, h = n % G::kHalves, ib = i & 1, nb = n % G::kVs;
         // (with two halves the next values would come too late behind this product, with one this
         // product behind the next values)
         bool next = st + 1 < subs || u < u1;
-        if (G::kHalves > 1 && next && __all_sync(~0u, mbar_test(B.op_full + op.i, op.ph))) {
+        if (G::kHalves > 1 && G::kVs > 1 && next && __all_sync(~0u, mbar_test(B.op_full + op.i, op.ph))) {
           v_ident(n + 1);
           next = false;
         }
-        wait2(B.v_full + nb, n >> 1, B.p_full + ib, i >> 1);
+        wait2(B.v_full + nb, n / G::kVs, B.p_full + ib, i >> 1);
         fence_after();
         if (elect_one()) {
           const uint64_t dP = sw128_desc(base + G::oP + ib * G::kP);
@@ -718,35 +720,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           }
         }
         if (move) {
-          // to the maxima over this step's 128 tokens
-          float y[RH];
-#pragma unroll
-          for (int k = 0; k < RH; ++k) y[k] = x[k] = x[k] * a.scale_log2;
-          const float w = warp_max_of<RH>(y);
+          // to the maxima over this step's 128 tokens (eight rows at a time: with 16 a warp is short
+          // of registers)
+          constexpr int C = RH < 8 ? RH : 8;
           float* hr = hred + (turn ^= 1) * 8 * RH;  // (the turn before may still be read)
-          if (lane < RH) hr[quad * RH + lane] = w;
-          soft_sync(half);
-          float f[RH];
 #pragma unroll
-          for (int k = 0; k < RH; ++k) {
-            const float d = fmaxf(fmaxf(hr[k], hr[RH + k]), fmaxf(hr[2 * RH + k], hr[3 * RH + k]));
-            const float old = m[k];
-            m[k] = fmaxf(old, d);
-            x[k] -= m[k];
-            f[k] = ex2(old - m[k]);
-            l[k] *= f[k];
+          for (int c = 0; c < RH; c += C) {
+            float y[C];
+#pragma unroll
+            for (int k = 0; k < C; ++k) y[k] = x[c + k] = x[c + k] * a.scale_log2;
+            const float w = warp_max_of<C>(y);
+            if (lane < C) hr[quad * RH + c + lane] = w;
           }
-          if (st > 0) {
-            // the sums so far, once no product adds to them
+          soft_sync(half);
+          if (st > 0) {  // the sums so far, once no product adds to them
             wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
             fence_after();
+          }
 #pragma unroll
-            for (int h = 0; h < G::kHalves; ++h) {
-              float o[RH];
-              tmem_ld<RH>(tl + G::cO + h * NM + k0, o);
+          for (int c = 0; c < RH; c += C) {
+            float f[C];
 #pragma unroll
-              for (int k = 0; k < RH; ++k) o[k] *= f[k];
-              tmem_st<RH>(tl + G::cO + h * NM + k0, o);
+            for (int k = 0; k < C; ++k) {
+              const float d = fmaxf(fmaxf(hr[c + k], hr[RH + c + k]), fmaxf(hr[2 * RH + c + k], hr[3 * RH + c + k]));
+              const float old = m[c + k];
+              m[c + k] = fmaxf(old, d);
+              x[c + k] -= m[c + k];
+              f[k] = ex2(old - m[c + k]);
+              l[c + k] *= f[k];
+            }
+            if (st > 0) {
+#pragma unroll
+              for (int h = 0; h < G::kHalves; ++h) {
+                float o[C];
+                tmem_ld<C>(tl + G::cO + h * NM + k0 + c, o);
+#pragma unroll
+                for (int k = 0; k < C; ++k) o[k] *= f[k];
+                tmem_st<C>(tl + G::cO + h * NM + k0 + c, o);
+              }
             }
           }
           numerators();
@@ -1068,14 +1079,14 @@ cudaError_t prepare() {
   static std::atomic<int> known[64];
   if (dev < 64 && known[dev].load(std::memory_order_acquire)) return cudaSuccess;
   e = cudaFuncSetAttribute(k_kv4_attn<D, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Geo<D, RN>::smem(kMaxReqs));
+                           (int)Geo<D, RN>::smem(Geo<D, RN>::kReqs));
   if (e == cudaSuccess && dev < 64) known[dev].store(1, std::memory_order_release);
   return e;
 }
 
 template <int D, int RN>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
-  static_assert(Geo<D, RN>::smem(kMaxReqs) <= 232448 - 256, "shared memory");
+  static_assert(Geo<D, RN>::smem(Geo<D, RN>::kReqs) <= 232448 - 256, "shared memory");
   cudaError_t e = prepare<D, RN>();
   if (e != cudaSuccess) return e;
   e = mtail::launch_k(k_kv4_attn<D, RN>, dim3(a.ctas), dim3(kThreads), Geo<D, RN>::smem(a.reqs), st, true, a);
@@ -1094,6 +1105,7 @@ cudaError_t dispatch(int D, int rn, F&& f) {
     case 12832: return f(std::integral_constant<int, 128>(), std::integral_constant<int, 32>());
     case 25608: return f(std::integral_constant<int, 256>(), std::integral_constant<int, 8>());
     case 25616: return f(std::integral_constant<int, 256>(), std::integral_constant<int, 16>());
+    case 25632: return f(std::integral_constant<int, 256>(), std::integral_constant<int, 32>());
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1102,7 +1114,7 @@ cudaError_t dispatch(int D, int rn, F&& f) {
 
 int attn_rows_per_item(int D, int G, int max_new) {
   const int64_t rows = (int64_t)G * max_new;
-  return rows <= 8 ? 8 : (rows <= 16 || D == 256) ? 16 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 
 int attn_ctas(int D, int rn, cudaError_t* err) {
@@ -1118,6 +1130,7 @@ size_t attn_workspace_bytes(int D, int rn, int ctas) {
 }
 
 cudaError_t launch_kv4_attention(const AttnArgs& a, int rn, cudaStream_t st) {
+  if (a.D == 256 && a.reqs > Geo<256, 32>::kReqs) rn = std::min(rn, 16);
   return dispatch(a.D, rn, [&](auto d, auto n) { return launch<decltype(d)::value, decltype(n)::value>(a, st); });
 }
 

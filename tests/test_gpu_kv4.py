@@ -345,7 +345,8 @@ def test_attention_many_rows(D, G, new):
 
 @pytest.mark.parametrize("D,G,heads,new,lens", [
     (64, 256, 1, 1, [70, 3]), (128, 1, 256, 1, [40]), (256, 1, 100, 1, [33, 1]), (64, 2, 255, 1, [18]),
-    (128, 4, 1, 513, [513]), (64, 1, 2, 400, [400, 1100])])
+    (128, 4, 1, 513, [513]), (64, 1, 2, 400, [400, 1100]), (256, 16, 1, 4, [900, 30, 2500]),
+    (256, 40, 2, 1, [300, 1300]), (256, 3, 1, 100, [640])])
 def test_attention_at_the_limits_of_heads_and_rows(D, G, heads, new, lens):
     s = Step(40, lens, new, G, heads, D, 16)
     s.check(s.run())
@@ -508,6 +509,12 @@ def test_long_context_is_split_and_joined(D, G, heads, L):
 def test_many_requests():
     rng = np.random.default_rng(21)
     s = Step(21, rng.integers(0, 90, 1024), 1, 4, 1, 64, 16, garbage=False)
+    s.check(s.run())
+
+
+def test_many_requests_of_many_wide_rows():
+    rng = np.random.default_rng(22)
+    s = Step(22, rng.integers(5, 60, 270), 5, 5, 1, 256, 16, garbage=False)
     s.check(s.run())
 
 
