@@ -694,8 +694,9 @@ def test_a_decode_run_into_the_layer_tail():
 
 
 def test_a_captured_decode_step_follows_the_lengths():
-    """One graph of a whole step, replayed while the lengths in device memory grow: the same bits as
-    the calls one by one on a second cache."""
+    """One graph of a whole step, replayed while the lengths in device memory grow, with requests that
+    pause (their rows go to the end of the step, a padded batch): the same bits as the calls one by
+    one on a second cache, and the padded rows stay."""
     R, hq, heads, D, page, width = 3, 16, 2, 128, 16, 20
     shape = gen.TailShape(R, 256, 8, 2, 128, 128, Ha=hq * D)
     d = gen.make_weights(shape, 4, keys=gen._LAYER_WEIGHTS + ("w_o",))
@@ -753,14 +754,18 @@ def test_a_captured_decode_step_follows_the_lengths():
     torch.cuda.synchronize()
     fresh = Side()
     prompts(fresh)
-    for name in ("cache", "table", "lens", "res", "free"):
+    for name in ("cache", "table", "lens", "res", "free", "out", "qkv", "y"):
         getattr(one, name).copy_(getattr(fresh, name))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         one.step()
     torch.cuda.synchronize()
     free = one.free.clone()
-    for step in range(8):
+    count = first.clone()
+    for step, active in enumerate(((1, 1, 1), (1, 0, 1), (0, 0, 0), (0, 1, 0), (1, 1, 1), (1, 1, 0), (1, 1, 1))):
+        new.copy_(torch.tensor(active, dtype=i32, device="cuda"))
+        count += new
+        before = one.out.clone()
         x = to_dev(normal_bits(rng, R, (hq + 2 * heads) * D))
         for side in (one, two):
             side.qkv.copy_(x)
@@ -771,7 +776,7 @@ def test_a_captured_decode_step_follows_the_lengths():
         for name in ("starts", "kv", "pos", "slots", "used", "table", "cache", "out", "res", "y", "lens"):
             assert torch.equal(getattr(one, name), getattr(two, name)), (step, name)
         assert int(one.st) == 0 and int(two.st) == 0
-        assert torch.equal(one.lens, first + step + 1)
+        assert torch.equal(one.lens, count) and torch.equal(one.out[sum(active):], before[sum(active):])
         free = torch.cat([free[int(one.used):], torch.full((int(one.used),), -1, dtype=i32, device="cuda")])
     assert tail.status() == 0
     tail.close()
