@@ -270,13 +270,24 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
     else __syncwarp();
     float cf[8], sf[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cf[e] = g[e], sf[e] = 0.f;
-      if (turns) {
-        const int f = a.interleaved ? 4 * li + e / 2 : 8 * (low ? li : other) + e;
-        const bool front = a.interleaved ? e % 2 == 0 : low;
-        cf[e] = g[e] * cosines[f];
-        sf[e] = (a.interleaved ? g[e ^ 1] : go[e]) * (front ? -sines[f] : sines[f]);
+    for (int e = 0; e < 8; ++e) cf[e] = g[e], sf[e] = 0.f;
+    if (turns && a.interleaved) {
+      const float4 co = *reinterpret_cast<const float4*>(cosines + 4 * li), si = *reinterpret_cast<const float4*>(sines + 4 * li);
+      const float cc[4] = {co.x, co.y, co.z, co.w}, ss[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        cf[e] = g[e] * cc[e / 2], cf[e + 1] = g[e + 1] * cc[e / 2];
+        sf[e] = g[e + 1] * -ss[e / 2], sf[e + 1] = g[e] * ss[e / 2];
+      }
+    } else if (turns) {
+      const int f = 8 * (low ? li : other);
+      const float sign = low ? -1.f : 1.f;
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4 co = *reinterpret_cast<const float4*>(cosines + f + e), si = *reinterpret_cast<const float4*>(sines + f + e);
+        cf[e] = g[e] * co.x, cf[e + 1] = g[e + 1] * co.y, cf[e + 2] = g[e + 2] * co.z, cf[e + 3] = g[e + 3] * co.w;
+        sf[e] = go[e] * (sign * si.x), sf[e + 1] = go[e + 1] * (sign * si.y);
+        sf[e + 2] = go[e + 2] * (sign * si.z), sf[e + 3] = go[e + 3] * (sign * si.w);
       }
     }
 #pragma unroll
