@@ -214,8 +214,10 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % L, gi = lane / L;
   // `blocks` CTAs to a row, which form its angles together, or (0) each warp for itself
   const int parts = qparts + kparts, w = blockIdx.x * 8 + warp;
-  const int row = blocks ? blockIdx.x / blocks : w / parts;
-  const int part = blocks ? w - row * blocks * 8 : w - row * parts;
+  // (there the queries' parts come first, the keys' shorter ones fill up at the end)
+  const int keys = w - a.rows * qparts;
+  const int row = blocks ? blockIdx.x / blocks : keys < 0 ? w / qparts : keys / max(kparts, 1);
+  const int part = blocks ? w - row * blocks * 8 : keys < 0 ? w - row * qparts : qparts + keys - row * kparts;
   mtail::pdl_trigger();
   mtail::pdl_wait();
   if (row >= a.rows) return;  // (the whole CTA where it works together)
