@@ -179,11 +179,11 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
 // y the scaled channel, y' its partner, cos' = gain cos, sin' = partner's gain times +-sin.  The
 // heads come through a ring in shared memory, kDepth asynchronous copies of 512 bytes ahead of
 // their use and the first of them while the angles are formed: in registers as many would leave
-// room for half the warps (three of them: 68 us, the ring 59).  8192 rows of 64 + 8 heads of 128 take
-// 59 us (302 MB, 5.1 TB/s, 0.75 of the measured copy rate), bounded by the instructions (issue slots
-// 77 % busy with single floats, before pairs of them were taken together); CTAs of one row each,
-// which form its angles together, take 69 there, but are what serves a few rows (2.6 us for one row,
-// 2.9 for 32 of D 256: launches).
+// room for half the warps (three of them: 68 us, the ring then 60).  8192 rows of 64 + 8 heads of 128
+// take 50 us (302 MB, 6.05 TB/s, 0.89 of the measured copy rate), of 128 + 8 heads 88 us (0.95):
+// memory, and below some 30 heads a row the angles' instructions.  CTAs of one row each, which form
+// its angles together, take 69 us there, but are what serves a few rows (2.4 us for one row, 2.9 for
+// 32 of D 256: launches).
 //
 // Angles: positions reach 2^31, where a product in 32 bits has lost the fraction of a turn and one
 // in fp64 is slow on this part.  So the frequency is taken in turns as a 64-bit binary fraction,
@@ -514,11 +514,11 @@ cudaError_t launch_step_tables(const TablesArgs& a, cudaStream_t st) {
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
   const int L = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, G = 32 / L;
-  // One head per lane group and warp until every SM has 48 warps, then up to 16, in equal parts: the
+  // One head per lane group and warp until every SM has 48 warps, then up to 32, in equal parts: the
   // angles are formed once per warp, and a ring is better used by a longer run (8192 rows of 64 + 8
-  // heads: 60 us with 16, 65 with 8, before the pairs of floats).
+  // heads: 61 us with 8, 53 with 16, 50 with 32 and with 64; of 128 + 8: 93, 88 and 92 with 16, 32, 64).
   const int64_t groups = (int64_t)a.rows * ((a.hq + a.hk + G - 1) / G), fill = (int64_t)num_sms() * 48;
-  const int most = G * (int)std::min<int64_t>(std::max<int64_t>(groups / fill, 1), 16);
+  const int most = G * (int)std::min<int64_t>(std::max<int64_t>(groups / fill, 1), 32);
   auto split = [&](int heads, int& parts) {
     parts = (heads + most - 1) / most;
     return parts ? ((heads + parts - 1) / parts + G - 1) / G * G : G;
