@@ -58,7 +58,8 @@ struct RowsArgs {
   int rows, heads, D, page;
   int64_t n_slots;      // n_pages * page
   uint64_t page_magic;  // ceil(2^64 / page): slot / page by a multiply
-  uint64_t head_magic;  // ceil(2^64 / heads) (of two heads and more)
+  int units;            // of a row's heads (set by the launch)
+  uint64_t unit_magic;  // ceil(2^64 / units) (of two units and more)
   uint8_t* cache;
   uint16_t* k;  // read by the append, written by the read
   uint16_t* v;

@@ -339,11 +339,11 @@ __global__ void __launch_bounds__(256, 4) k_qk_norm_rope(const RopeArgs a, int q
 //
 // D/8 lanes hold one token's head, eight channels each, of its keys and of its values, so that a
 // block of 32 channels is four neighbouring lanes: its largest magnitude is two shuffles, and a
-// lane's eight codes are one word.  65537 rows of 8 heads of 128: in 68 us (5.0 TB/s over 340 MB, 0.73
-// of the measured copy rate; the instructions bound it, issue slots were 78 % busy at 75 us), out 61
-// us (5.5 TB/s, 0.82); 32 rows in and out 3.4 us, two launches.  A
-// token's bytes lie in 8- and 1-byte pieces all over its tile, so partial sectors reach the L2; tiles
-// put together in shared memory first took 103 us, as the two more barriers cost more than the sectors.
+// lane's eight codes are one word.  65537 rows of 8 heads of 128: in 57 us (5.9 TB/s over 340 MB, 0.87
+// of the measured copy rate; with a look-up for each head it took 68, instructions), out 61 us (5.6
+// TB/s, 0.82); 32 rows in and out 3.3 us, two launches.  A token's bytes lie in 8- and 1-byte pieces all
+// over its tile, so partial sectors reach the L2; tiles put together in shared memory first took 103 us
+// (75 then), as the two more barriers cost more than the sectors.
 
 template <int D>
 __device__ __forceinline__ uint8_t* tile_of(const RowsArgs& a, int64_t slot, int h) {
@@ -352,9 +352,13 @@ __device__ __forceinline__ uint8_t* tile_of(const RowsArgs& a, int64_t slot, int
   const int off = (int)(slot - page * a.page);
   return a.cache + ((page * a.heads + h) * (a.page / 16) + off / 16) * (17 * D);
 }
-__device__ __forceinline__ uint32_t row_of(const RowsArgs& a, uint32_t id) {  // id / heads
-  return a.heads == 1 ? id : (uint32_t)__umul64hi(id, a.head_magic);
+// A group of lanes takes `units` a row: heads h, h + units, .. of kPairs, whose loads overlap and which
+// share the row's look-up.
+__device__ __forceinline__ uint32_t row_of(const RowsArgs& a, uint32_t id) {  // id / units
+  return a.units == 1 ? id : (uint32_t)__umul64hi(id, a.unit_magic);
 }
+template <int D>
+__device__ __forceinline__ int64_t next_tile(const RowsArgs& a) { return (int64_t)a.units * (a.page / 16) * (17 * D); }
 // byte n of lane l of a tile's codes
 __device__ __forceinline__ int lane_byte(int n, int l) { return (n >> 4) * 512 + l * 16 + (n & 15); }
 
@@ -386,65 +390,69 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t* scale) {
   return mtail::e2m1x8_pack(x);
 }
 
-// kPairs (row, head) pairs per group of lanes, here and in the read: their loads overlap.
 template <int D, int kPairs>
 __global__ void __launch_bounds__(256) k_kv4_append(const RowsArgs a) {
   constexpr int L = D / 8, NB = D / 32;
-  const uint32_t id0 = blockIdx.x * (kPairs * 256 / L) + threadIdx.x / L;  // (row, head); at most 2^32
+  const uint32_t id = blockIdx.x * (256 / L) + threadIdx.x / L;  // (row, unit); at most 2^32
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
   mtail::pdl_trigger();
   mtail::pdl_wait();
-  uint32_t h[kPairs];
-  int64_t slot[kPairs];
+  const uint32_t row = row_of(a, id), h = id - row * (uint32_t)a.units;
+  int64_t slot = -1;
   uint4 ku[kPairs], vu[kPairs];
 #pragma unroll
-  for (int p = 0; p < kPairs; ++p) {
-    const uint32_t id = id0 + p * (256 / L), row = row_of(a, id);
-    h[p] = id - row * (uint32_t)a.heads;
-    slot[p] = -1;
-    ku[p] = vu[p] = make_uint4(0, 0, 0, 0);
-    if (row < (uint32_t)a.rows) {  // (the loads need not wait for the slot)
-      slot[p] = a.slots[row];
-      ku[p] = *(reinterpret_cast<const uint4*>(a.k + row * a.ldk + h[p] * D) + i);
-      vu[p] = *(reinterpret_cast<const uint4*>(a.v + row * a.ldv + h[p] * D) + i);
-    }
+  for (int p = 0; p < kPairs; ++p) ku[p] = vu[p] = make_uint4(0, 0, 0, 0);
+  if (row < (uint32_t)a.rows) {  // (the loads need not wait for the slot)
+    slot = a.slots[row];
+    const uint16_t* k = a.k + row * a.ldk + h * D + 8 * i;
+    const uint16_t* v = a.v + row * a.ldv + h * D + 8 * i;
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p)
+      if (p == 0 || h + p * a.units < (uint32_t)a.heads) {
+        ku[p] = *reinterpret_cast<const uint4*>(k + p * a.units * D);
+        vu[p] = *reinterpret_cast<const uint4*>(v + p * a.units * D);
+      }
   }
+  if (slot >= a.n_slots) {
+    if (h == 0 && i == 0) report(a.status, kStatusBadSlot);
+    slot = -1;
+  }
+  const int t = (int)(slot & 15);  // (a page is a multiple of 16 tokens)
+  uint8_t* tile = slot >= 0 ? tile_of<D>(a, slot, (int)h) : a.cache;
+  // this lane's places in the tile: its key codes, the key scales of up to four blocks, the value codes
+  // of lanes (b, c), b = 0, 1 and the value scale
+  const int kc = lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c);
+  const int ksc = 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB + (NB == 2 ? 0 : b);
+  const int vc = 8 * D + lane_byte(((t >> 3) * 2 + (t & 1)) * (D / 16), (2 * c + b) * 4 + ((t & 7) >> 1));
+  const int vsc = 16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1);
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) {
-    if (slot[p] >= a.n_slots) {
-      if (h[p] == 0 && i == 0) report(a.status, kStatusBadSlot);
-      slot[p] = -1;
-    }
     uint32_t ks, vs;
     const uint32_t kw = quantize8(ku[p], &ks), vw = quantize8(vu[p], &vs);
-    // the key scales of up to four blocks in one store
     uint32_t sw = ks << (8 * (b & 3));
     sw |= __shfl_xor_sync(~0u, sw, 4);
     if (NB > 2) sw |= __shfl_xor_sync(~0u, sw, 8);
-    // lanes (b, c), b = 0, 1 collect the 16-bit pieces of every block of the values for g = 2c + b
+    // the 16-bit pieces of every block of the values for g = 2c + b
     uint32_t vv[4];
 #pragma unroll
     for (int k = 0; k < NB / 2; ++k) {
       const uint32_t w0 = __shfl_sync(~0u, vw, 8 * k + c, L), w1 = __shfl_sync(~0u, vw, 8 * k + 4 + c, L);
       vv[k] = b == 0 ? __byte_perm(w0, w1, 0x5410) : __byte_perm(w0, w1, 0x7632);
     }
-    if (slot[p] < 0) continue;  // (before the next pair's shuffles the warp is together again)
-    const int t = (int)(slot[p] & 15);  // (a page is a multiple of 16 tokens)
-    uint8_t* tile = tile_of<D>(a, slot[p], (int)h[p]);
-    *reinterpret_cast<uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c)) = kw;
-    if (c == 0 && (b & 3) == 0) {
-      uint8_t* s = tile + 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB;
-      if (NB == 2) *reinterpret_cast<uint16_t*>(s) = (uint16_t)sw;
-      else *reinterpret_cast<uint32_t*>(s + b) = sw;
+    if (slot >= 0 && (p == 0 || h + p * a.units < (uint32_t)a.heads)) {
+      uint8_t* to = tile + p * next_tile<D>(a);
+      *reinterpret_cast<uint32_t*>(to + kc) = kw;
+      if (c == 0 && (b & 3) == 0) {
+        if (NB == 2) *reinterpret_cast<uint16_t*>(to + ksc) = (uint16_t)sw;
+        else *reinterpret_cast<uint32_t*>(to + ksc) = sw;
+      }
+      if (b < 2) {
+        if constexpr (NB == 2) *reinterpret_cast<uint32_t*>(to + vc) = vv[0];
+        else if constexpr (NB == 4) *reinterpret_cast<uint2*>(to + vc) = make_uint2(vv[0], vv[1]);
+        else *reinterpret_cast<uint4*>(to + vc) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
+      }
+      if (c == 0) to[vsc] = (uint8_t)vs;
     }
-    if (b < 2) {
-      uint8_t* q = tile + 8 * D +
-                   lane_byte(((t >> 3) * 2 + (t & 1)) * (D / 16), (2 * c + b) * 4 + ((t & 7) >> 1));
-      if constexpr (NB == 2) *reinterpret_cast<uint32_t*>(q) = vv[0];
-      else if constexpr (NB == 4) *reinterpret_cast<uint2*>(q) = make_uint2(vv[0], vv[1]);
-      else *reinterpret_cast<uint4*>(q) = make_uint4(vv[0], vv[1], vv[2], vv[3]);
-    }
-    if (c == 0) tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)] = (uint8_t)vs;
   }
 }
 
@@ -465,40 +473,39 @@ __device__ __forceinline__ uint4 dequantize8(uint32_t w, uint32_t s) {
 template <int D, int kPairs>
 __global__ void __launch_bounds__(256) k_kv4_read(const RowsArgs a) {
   constexpr int L = D / 8, NB = D / 32;
-  const uint32_t id0 = blockIdx.x * (kPairs * 256 / L) + threadIdx.x / L;
+  const uint32_t id = blockIdx.x * (256 / L) + threadIdx.x / L;
   const int i = threadIdx.x % L, b = i >> 2, c = i & 3;
   mtail::pdl_trigger();
   mtail::pdl_wait();
-  uint32_t row[kPairs], h[kPairs], kw[kPairs], vw[kPairs], ks[kPairs], vs[kPairs];
-  int64_t slot[kPairs];
+  const uint32_t row = row_of(a, id), h = id - row * (uint32_t)a.units;
+  if (row >= (uint32_t)a.rows) return;
+  const int64_t slot = a.slots[row];
+  if (slot >= a.n_slots && h == 0 && i == 0) report(a.status, kStatusBadSlot);
+  if (slot < 0 || slot >= a.n_slots) return;
+  const int t = (int)(slot & 15);
+  const uint8_t* tile = tile_of<D>(a, slot, (int)h);
+  const int kc = lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c);
+  const int ksc = 16 * D + (t & 7) * (D / 16) + (t >> 3) * NB + b;
+  const int n = ((t >> 3) * 2 + (t & 1)) * (D / 16) + 2 * b;
+  const int vc0 = 8 * D + lane_byte(n, 8 * c + ((t & 7) >> 1)), vc1 = 8 * D + lane_byte(n, 8 * c + 4 + ((t & 7) >> 1));
+  const int vsc = 16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1);
+  uint32_t kw[kPairs], vw[kPairs], ks[kPairs], vs[kPairs];
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) {
-    const uint32_t id = id0 + p * (256 / L);
-    row[p] = row_of(a, id), h[p] = id - row[p] * (uint32_t)a.heads;
-    slot[p] = row[p] < (uint32_t)a.rows ? a.slots[row[p]] : -1;
+    if (p > 0 && h + p * a.units >= (uint32_t)a.heads) continue;
+    const uint8_t* at = tile + p * next_tile<D>(a);
+    kw[p] = *reinterpret_cast<const uint32_t*>(at + kc);
+    ks[p] = at[ksc];
+    vw[p] = *reinterpret_cast<const uint16_t*>(at + vc0) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + vc1) << 16;
+    vs[p] = at[vsc];
   }
+  uint16_t* k = a.k + row * a.ldk + h * D + 8 * i;
+  uint16_t* v = a.v + row * a.ldv + h * D + 8 * i;
 #pragma unroll
   for (int p = 0; p < kPairs; ++p) {
-    if (slot[p] >= a.n_slots) {
-      if (h[p] == 0 && i == 0) report(a.status, kStatusBadSlot);
-      slot[p] = -1;
-    }
-    if (slot[p] < 0) continue;
-    const int t = (int)(slot[p] & 15);
-    const uint8_t* tile = tile_of<D>(a, slot[p], (int)h[p]);
-    kw[p] = *reinterpret_cast<const uint32_t*>(tile + lane_byte((t >> 3) * (D / 8) + 4 * b, (t & 7) * 4 + c));
-    ks[p] = tile[16 * D + (t & 7) * (D / 16) + (t >> 3) * NB + b];
-    const uint8_t* v = tile + 8 * D;
-    const int n = ((t >> 3) * 2 + (t & 1)) * (D / 16) + 2 * b;
-    vw[p] = *reinterpret_cast<const uint16_t*>(v + lane_byte(n, 8 * c + ((t & 7) >> 1))) |
-            (uint32_t)*reinterpret_cast<const uint16_t*>(v + lane_byte(n, 8 * c + 4 + ((t & 7) >> 1))) << 16;
-    vs[p] = tile[16 * D + D / 2 + ((t & 7) >> 1) * (D / 8) + 4 * b + (t >> 3) * 2 + (t & 1)];
-  }
-#pragma unroll
-  for (int p = 0; p < kPairs; ++p) {
-    if (slot[p] < 0) continue;
-    *(reinterpret_cast<uint4*>(a.k + row[p] * a.ldk + h[p] * D) + i) = dequantize8(kw[p], ks[p]);
-    *(reinterpret_cast<uint4*>(a.v + row[p] * a.ldv + h[p] * D) + i) = dequantize8(vw[p], vs[p]);
+    if (p > 0 && h + p * a.units >= (uint32_t)a.heads) continue;
+    *reinterpret_cast<uint4*>(k + p * a.units * D) = dequantize8(kw[p], ks[p]);
+    *reinterpret_cast<uint4*>(v + p * a.units * D) = dequantize8(vw[p], vs[p]);
   }
 }
 
@@ -536,9 +543,11 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st) {
 
 namespace {
 template <bool kAppend, int kPairs>
-cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
-  const int per = kPairs * 256 / (a.D / 8);                       // pairs of a CTA
-  const int64_t n = ((int64_t)a.rows * a.heads + per - 1) / per;  // <= 2^24 * 256 / 8
+cudaError_t launch_rows(RowsArgs a, cudaStream_t st) {
+  a.units = (a.heads + kPairs - 1) / kPairs;
+  a.unit_magic = ~0ull / (uint64_t)a.units + 1;
+  const int per = 256 / (a.D / 8);                                // units of a CTA
+  const int64_t n = ((int64_t)a.rows * a.units + per - 1) / per;  // <= 2^24 * 256 / 8
   auto* kernel = a.D == 64    ? (kAppend ? k_kv4_append<64, kPairs> : k_kv4_read<64, kPairs>)
                  : a.D == 128 ? (kAppend ? k_kv4_append<128, kPairs> : k_kv4_read<128, kPairs>)
                               : (kAppend ? k_kv4_append<256, kPairs> : k_kv4_read<256, kPairs>);
@@ -546,10 +555,12 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
 }
 template <bool kAppend>
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
-  // One pair a group of lanes until the GPU is filled several times over (32 rows of 8 heads, in and
-  // out: 3.6 us, with two 4.5), then two (65537 rows: 127 us).
+  // One head a group of lanes until the GPU is filled several times over (32 rows of 8 heads, in and
+  // out: 3.3 us, with two 4.5), then more where a row has them (65537 rows of 8 heads: in 60 us with two
+  // and 57 with four, out 61 and 64).
   const int64_t threads = (int64_t)a.rows * a.heads * (a.D / 8);
-  return threads < (int64_t)num_sms() * 2048 * 4 ? launch_rows<kAppend, 1>(a, st) : launch_rows<kAppend, 2>(a, st);
+  if (threads < (int64_t)num_sms() * 2048 * 4 || a.heads < 2) return launch_rows<kAppend, 1>(a, st);
+  return kAppend && a.heads % 4 == 0 ? launch_rows<kAppend, 4>(a, st) : launch_rows<kAppend, 2>(a, st);
 }
 }  // namespace
 

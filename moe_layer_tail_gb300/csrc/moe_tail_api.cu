@@ -729,7 +729,6 @@ int kv4_rows(bool append, int32_t rows, int32_t kv_heads, int32_t head_dim, int3
   a.page = page_size;
   a.n_slots = n_pages * page_size;
   a.page_magic = ~0ull / (uint64_t)page_size + 1;  // (page_size >= 16; 2^64 / 2^k comes out exact)
-  a.head_magic = ~0ull / (uint64_t)kv_heads + 1;
   a.cache = (uint8_t*)cache;
   a.k = (uint16_t*)k;
   a.v = (uint16_t*)v;

@@ -100,6 +100,30 @@ def test_rows_side_by_side_in_their_tiles(D, heads):
     assert np.array_equal(cache.cpu().numpy(), expect) and int(st) == mt.KV4_STATUS_BAD_SLOT
 
 
+@pytest.mark.parametrize("D,heads,rows", [(64, 1, 21000), (128, 5, 17000), (128, 8, 9800), (256, 3, 13001),
+                                          (64, 12, 13100)])
+def test_rows_that_fill_the_gpu(D, heads, rows):
+    # enough rows for the forms that take several heads of a row together; rows without a slot between
+    rng = np.random.default_rng([D, heads, rows])
+    page = 64
+    pages = -(-rows // page) + 1
+    slots = rng.permutation(pages)[np.arange(rows) // page] * page + np.arange(rows) % page
+    slots[rng.random(rows) < 0.01] = -1
+    at = torch.from_numpy(slots.astype(np.int64)).cuda()
+    k, v = (torch.from_numpy(normal_bits(rng, rows, heads, D).view(np.int16)).cuda().view(BF) for _ in range(2))
+    one, two = mt.kv4_cache(pages, page, heads, D), mt.kv4_cache(pages, page, heads, D)
+    st = status_word()
+    mt.kv4_append(one, k, v, at, status=st)
+    for r in range(0, rows, 200):  # (small calls take another form, checked above)
+        mt.kv4_append(two, k[r:r + 200], v[r:r + 200], at[r:r + 200], status=st)
+    assert torch.equal(one, two) and int(one.count_nonzero()) > 0
+    outs = [[torch.full((rows, heads, D), 7.0, dtype=BF, device="cuda") for _ in range(2)] for _ in range(2)]
+    mt.kv4_read(one, at, *outs[0], status=st)
+    for r in range(0, rows, 200):
+        mt.kv4_read(one, at[r:r + 200], *(o[r:r + 200] for o in outs[1]), status=st)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1]) and int(st) == 0
+
+
 def test_rows_without_a_slot_are_left_alone():
     rng = np.random.default_rng(1)
     before = rng.integers(0, 256, (2, 2, 1, 17 * 64), dtype=np.uint8)
