@@ -25,6 +25,7 @@ enum : int32_t {
 
 struct TablesArgs {
   int reqs, max_rows, page, n_free, width;
+  uint64_t page_magic;  // ceil(2^64 / page): a length / page by a multiply
   int64_t stride;
   const int32_t* cached;
   const int32_t* fresh;

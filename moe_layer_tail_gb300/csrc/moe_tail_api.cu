@@ -762,6 +762,7 @@ extern "C" int moe_step_tables(int32_t reqs, int32_t max_rows, int32_t page_size
   a.reqs = reqs;
   a.max_rows = max_rows;
   a.page = page_size;
+  a.page_magic = ~0ull / (uint64_t)page_size + 1;
   a.n_free = n_free;
   a.width = table_width;
   a.stride = table_stride;
