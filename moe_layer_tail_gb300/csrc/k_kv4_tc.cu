@@ -36,12 +36,13 @@
 // softmax.  Tensor memory is full at D 128 (K' 128 columns, V' 2 x 128, S, O, scales of 512), so
 // neither can run further ahead.  Tried and slower at this size: K' in a ring of three blocks of 64
 // channels with a warp of its own (163 us: six runs of products a step instead of four, and each
-// costs the pipe some 150 cycles beside its products); both dequantisations in one run (160); V'
-// and K' in halves (234); waits that poll (185; a dozen polling warps take the shared-memory pipe
-// from the others); one group of four softmax warps (190).  D 64 has the same chains for half the
-// bytes (K' twice there changed nothing); D 256 twice the products for its two halves of channels:
-// four rows of eight requests of up to 16384 tokens, 64 rows a kv head, take 71 us in two items of 32
-// rows and took 103 in four of 16.
+// costs the pipe some 150 cycles beside its products); both dequantisations in one run (160); a warp
+// of its own for V' (141: its products get in front of the scores' in the pipe), V' before the output
+// product (140); V' and K' in halves (234); waits that poll (185; a dozen polling warps take the
+// shared-memory pipe from the others); one group of four softmax warps (190).  D 64 has the same
+// chains for half the bytes (K' twice there changed nothing); D 256 twice the products for its two
+// halves of channels: four rows of eight requests of up to 16384 tokens, 64 rows a kv head, take 71
+// us in two items of 32 rows and took 103 in four of 16.
 //
 // Warps: 0 looks up pages and copies tiles (bulk copies into a ring, 32 look-ups at a time);
 // 6..13 (one per tile of a step) bring a tile's bytes, which the cache holds in the order of
