@@ -280,14 +280,14 @@ __device__ __forceinline__ float warp_sum_of(float (&v)[N]) {
   return v[0];
 }
 
-// Waits in hardware for up to 0.2 ms (without the hint a waiting warp polls, and a dozen of them
-// take the shared-memory pipe from the others).
+// Waits in hardware for up to 20 us (without the hint a waiting warp polls, and a dozen of them take
+// the shared-memory pipe from the others; once a wait has given up, the others cost as long each).
 __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
       : "=r"(ok)
-      : "r"(smem_u32(b)), "r"(parity), "r"(200000u)
+      : "r"(smem_u32(b)), "r"(parity), "r"(20000u)
       : "memory");
   return ok != 0;
 }
