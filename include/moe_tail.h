@@ -302,6 +302,13 @@ int moe_tail_route_noalloc(const void* x, const void* residual, const void* gamm
  * tests; the pages have no counterpart. */
 int moe_tail_debug_timeline(moe_tail_t* h, uint64_t* stamps, int32_t n);
 
+/* For failure tests of moe_kv4_attention (kv4_attn.h) only: in this thread's next such call that is
+ * not refused, hand-over number `barrier` of its first CTA expects one arrival more than is ever sent,
+ * so that whoever waits for it gives up (after some 0.1 s; MOE_TAIL_STATUS_TIMEOUT in the call's
+ * status).  Numbers count the barriers of a CTA from 0; one past them, or one that the call's sizes
+ * never wait for, changes nothing; a negative one takes the order back.  Returns MOE_TAIL_OK. */
+int moe_tail_debug_kv4_stall(int32_t barrier);
+
 /* Re-make the handle's copy of w13_scales and w2_scales (see moe_tail_weights_t) from the
  * borrowed arrays, enqueued on `stream` (a cudaStream_t; NULL = legacy default stream):
  * later runs on that stream read the new scales.  A no-op returning MOE_TAIL_OK for forms

@@ -90,6 +90,7 @@ struct AttnArgs {
   int64_t ldo;
   float* part;  // workspace: [2 ctas][RN][D] averages, then [2 ctas][RN][2] (max, sum)
   int ctas;
+  int stall;  // failure tests: a barrier of CTA 0 that expects one arrival more than is sent (negative: none)
   int32_t* status;
 };
 // Query rows of one work item for calls with up to `max_new` rows of a request.

@@ -50,8 +50,9 @@
 // 1 issues K' and S, 14 V' and O (an elected thread each: a divergent issuer costs 45 cycles an
 // instruction, an elected one 9 at these sizes); 2..5 and 15..18 are the softmax and the output of
 // the lower and the upper half of the rows.  They hand over through mbarriers; every wait is bounded
-// and reports MOE_TAIL_STATUS_TIMEOUT.  Spills must stay out of the steps: local memory shares what
-// little L1 the 150..210 KB of shared memory leave, and versions that spilled took 2.5 times as long.
+// and reports MOE_TAIL_STATUS_TIMEOUT; a CTA in which one has given up ends without its results.  Spills
+// must stay out of the steps: local memory shares what little L1 the 150..210 KB of shared memory leave,
+// and versions that spilled took 2.5 times as long.
 //
 // Tensor memory is taken whole (512 columns) before the previous kernel in the stream has ended.
 // That cannot lock up: no other tensor-memory kernel of this library fits beside a CTA of this one
@@ -82,7 +83,7 @@ constexpr int kWarps = 19, kThreads = 32 * kWarps;
 constexpr int kLayWarp = 6, kValWarp = 14, kSoft2Warp = 15;
 constexpr int kStepTiles = 8;
 constexpr int kInfos = 8;                     // steps whose notes are kept
-constexpr int64_t kBudgetClocks = 200000000;  // of a wait, about 0.1 s
+constexpr uint32_t kBudgetClocks = 200000000;  // of a wait, about 0.1 s
 constexpr float kLow = -3.0e38f;              // a row's reference before its first score
 constexpr float kOver = 40.f;                 // octaves above the reference that move it
 
@@ -129,9 +130,9 @@ struct Geo {
   static constexpr int oSfI = oSf + kOps * kSf, oInfo = oSfI + 512;
   static constexpr int oSmall = oInfo + kInfos * (int)sizeof(Info);
   // raw and operand rings, info ring, q, and the single ones
-  static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 12 + 4;
+  static constexpr int kBars = 2 * kRaw + 2 * kOps + kInfos + 4 + 12 + 4 + 2;
   static constexpr int kSmall = kBars * 8 + kRaw * 20 * 4 /* t0, full */ + 4 * RN * 12 /* red, l */ +
-                                RN * 16 /* rowpos, nan */ + 64 + 32 /* over */;
+                                RN * 16 /* rowpos, nan */ + 64 /* checks */;
   static constexpr size_t smem(int reqs) {
     return 1024 + (size_t)oSmall + kSmall + (size_t)(3 * reqs + 2) * 4;
   }
@@ -238,8 +239,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float to_tf32(float x) {
   return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xFFFFE000u);
 }
-// the four softmax warps of one half of the rows
-__device__ __forceinline__ void soft_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 // bytes of w that are 255, one bit each
 __device__ __forceinline__ uint32_t ff_bytes(uint32_t w) {
   const uint32_t f = ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
@@ -303,7 +302,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
 
 struct Bars {
   uint64_t *raw_full, *raw_empty, *op_full, *op_empty, *info, *q_full, *q_empty;
-  uint64_t *k_full, *k_free, *s_full, *p_full, *v_full, *v_free, *pv, *soft;
+  uint64_t *k_full, *k_free, *s_full, *p_full, *v_full, *v_free, *pv, *soft, *meet;
 };
 
 // The record that tells the joining launch which item crosses the end of a range.
@@ -343,12 +342,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   B.v_free = B.v_full + 2;  // (two halves only)
   B.pv = B.v_free + 2;
   B.soft = B.pv + 2;
+  B.meet = B.soft + 4;
   int* raw_info = reinterpret_cast<int*>(bp + G::kBars);  // [kRaw][20]: t0 of the tiles, full
   float* red = reinterpret_cast<float*>(raw_info + G::kRaw * 20);  // [2][4][RN]
   float* lsum = red + 8 * RN;                                       // [4][RN]
   int* rowpos = reinterpret_cast<int*>(lsum + 4 * RN);
   uint32_t* nanrow = reinterpret_cast<uint32_t*>(rowpos + 2 * RN);  // both [2 turns][RN]
-  uint32_t* pre = nanrow + 2 * RN + 16;
+  // what the softmax warps ask for once a step, [half][turn]: a byte each, whether its scores passed
+  // kOver, and a word that tells them that a wait has given up
+  uint32_t* checks = nanrow + 2 * RN;
+  uint32_t* pre = checks + 16;
   int* lens = reinterpret_cast<int*>(pre + a.reqs + 1);
   int* starts = lens + a.reqs;
 
@@ -358,10 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   // ---- set-up that depends on nothing (it may run while the previous kernel ends), then the plan
   if (tid == 0) {
     s_dead = 0;
+    for (int i = 0; i < 8; ++i) checks[i] = 0;
     for (int i = 0; i < G::kBars; ++i) {
       uint64_t* b = bp + i;
       const bool lay = (b >= B.raw_empty && b < B.op_empty) || (b >= B.info && b < B.q_empty);
-      mbar_init(b, lay ? 8u : b >= B.op_empty && b < B.info ? 2u : b >= B.p_full && b < B.v_full ? 8u : b >= B.soft ? 4u : 1u);
+      const uint32_t n = lay ? 8u : b >= B.op_empty && b < B.info ? 2u : b >= B.p_full && b < B.v_full ? 8u : b >= B.soft ? 4u : 1u;
+      mbar_init(b, n + (blockIdx.x == 0 && i == a.stall));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -400,18 +405,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
   if (u0 == u1 && tid == 0) recs[blockIdx.x].last = -1;
 
-  bool gone = false;  // a wait gave up, here or elsewhere in the CTA
+  // A wait gave up, here or elsewhere in the CTA (of each lane: a warp asks for it by a vote).  From then
+  // on a wait takes one sleep at most and every role leaves its loops where it next asks; the
+  // softmax and the layout ask in what they read anyway, which warp 0 marks as it leaves.  What a warp
+  // still does then may differ from the others', so none waits for another but at these barriers, and
+  // all reach the kernel's last.  (Small code: a variable that lives through the steps of all
+  // roles, or a longer way out of each wait, cost 4 to 25 % of a long call; this 2 %.)
+  bool gone = false;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (mbar_test(b, parity & 1)) return;  // (quicker than the waiting form where it has completed)
-    const int64_t t0 = clock64();
+    const uint32_t t0 = clock();
     while (!mbar_sleep_wait(b, parity & 1)) {
-      gone = *reinterpret_cast<volatile int*>(&s_dead) != 0;
-      if (!gone && clock64() - t0 > kBudgetClocks) {
-        gone = true;
+      if (*reinterpret_cast<volatile int*>(&s_dead) || (uint32_t)clock() - t0 > kBudgetClocks) {
         *reinterpret_cast<volatile int*>(&s_dead) = 1;
-        if (a.status) atomicOr(a.status, kStatusTimeout);
+        gone = true;
+        return;
       }
-      if (gone) return;
     }
   };
   // both, asked for together
@@ -421,6 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     if (!d1) wait(b1, p1);
     __syncwarp();
   };
+  // in front of what a warp does together
+  auto wait1 = [&](uint64_t* b, uint32_t parity) {
+    wait(b, parity);
+    __syncwarp();
+  };
+  auto dead = [&]() { return __any_sync(~0u, *reinterpret_cast<volatile int*>(&s_dead)) != 0; };
   const int r0 = u0 < u1 ? find_req(pre, a.reqs, u0) : 0;
 
   if (warp == 0) {
@@ -432,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       r = s.r;
       const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first);
       const int pmin = s.q.L - s.q.nq + first / a.G, pmax = s.q.L - s.q.nq + (first + nrow - 1) / a.G;
-      for (int k = s.k0; k < s.k1; k += 32) {
+      for (int k = s.k0; k < s.k1 && !dead(); k += 32) {
         // a lane looks up one of 32 tiles, the copies of four steps
         const int kk = k + lane, tile = kk < s.q.ns ? kk : kk + s.q.off;
         int64_t at = -1;
@@ -455,17 +470,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           const uint32_t mine = have >> (8 * q) & 255;
           if (lane >> 3 == q) raw_info[st * 20 + (lane & 7)] = at >= 0 ? t0 : -1, raw_info[st * 20 + 8 + (lane & 7)] = full;
           __syncwarp();
-          const bool go = !__any_sync(~0u, gone);
+          if (__any_sync(~0u, gone)) break;
           if (lane == 0) {
-            if (mine && go) mbar_expect_tx(B.raw_full + st, __popc(mine) * G::kTile);
+            if (mine) mbar_expect_tx(B.raw_full + st, __popc(mine) * G::kTile);
             else mbar_arrive(B.raw_full + st);
           }
           __syncwarp();
-          if (lane >> 3 == q && at >= 0 && go)
+          if (lane >> 3 == q && at >= 0)
             bulk_load(dst + (lane & 7) * G::kTile, a.cache + at, G::kTile, B.raw_full + st);
         }
       }
       u += s.places;
+      if (dead()) break;
+    }
+    if (dead() && lane == 0) {  // (the softmax's checks, the tiles' full marks)
+      for (int i = 1; i < 8; i += 2) *reinterpret_cast<volatile uint32_t*>(checks + i) = 1;
+      for (int i = 0; i < G::kRaw * 8; ++i) *reinterpret_cast<volatile int*>(raw_info + (i >> 3) * 20 + 8 + (i & 7)) = 0;
     }
   } else if (warp == 1) {
     // --------------------------------------- the tensor cores: K' = K I, S^T = K' Q^T ----
@@ -485,11 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
       // the operands, and the scores of the sub-step before: the keys are used up
       if (G::kHalves > 1) {
         if (h == 0) wait(B.op_full + op.i, op.ph);
-        wait(B.k_free, n + 1);
+        wait1(B.k_free, n + 1);
       } else if (n > 0) {
         wait2(B.op_full + op.i, op.ph, B.s_full + ((n - 1) & 1), (n - 1) >> 1);
       } else {
-        wait(B.op_full + op.i, op.ph);
+        wait1(B.op_full + op.i, op.ph);
       }
       fence_after();
       if (elect_one()) {
@@ -614,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     const int quad = warp & 3;                       // tensor-memory lanes 32 quad ..
     const uint32_t tl = tm + ((uint32_t)quad << 21);  // (lane in bits 16..)
     const int tok = 32 * quad + lane;                // this thread's token of a step
-    uint8_t* over = reinterpret_cast<uint8_t*>(nanrow + 2 * RN) + half * 8;  // [2][4]: a warp's x passed kOver
+    uint32_t* check = checks + 4 * half;
     // where this token's numerators of rows k0 + k go (k and k + 8 lie 1024 bytes apart)
     uint8_t* ps[RH < 8 ? RH : 8];
 #pragma unroll
@@ -623,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     float* hred = red + half * 4 * RH;  // [2 turns][2 halves][4][RH]
     float* hsum = lsum + half * 4 * RH;
     int turn = 0, part = 0;
-    uint32_t i = 0, checks = 0;
+    uint32_t i = 0, nchecks = 0, meets = 0;
     Seg s;
     int first = 0, nrow = 0;
     auto open = [&](int r, uint32_t u) {  // the part from u on, its rows' positions
@@ -635,9 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         nanrow[(part & 1) * RN + k] = 0;
       }
     };
+    auto meet = [&]() {  // the four warps of this half: each sees what the others have stored
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B.meet + half);
+      wait1(B.meet + half, meets++);
+    };
     if (u0 < u1) open(r0, u0);
-    soft_sync(half);
-    for (uint32_t u = u0; u < u1; ++part) {
+    meet();
+    for (uint32_t u = u0; u < u1 && !dead(); ++part) {
       const int* rowp = rowpos + (part & 1) * RN + k0;
       uint32_t* nanr = nanrow + (part & 1) * RN + k0;
       const int steps = (s.k1 - s.k0 + kStepTiles - 1) / kStepTiles;
@@ -648,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         const uint32_t b = i & 1;
         const Info& inf = infos[i % kInfos];
         const uint32_t sa = tl + G::cS + b * NM + k0;
-        wait(B.s_full + b, i >> 1);
+        wait1(B.s_full + b, i >> 1);
         fence_after();
         // the notes of the step, and the product that read the numerators before these (both are
         // there by now as a rule: their tests run beside the load)
@@ -685,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           }
         }
         bool move = st == 0;  // the rows' references move
-        const uint32_t cb = checks & 1;
+        const uint32_t cb = nchecks & 1;
         if (!move) {
           float top = -INFINITY;
 #pragma unroll
@@ -695,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
           }
           const bool mine = __any_sync(~0u, top > kOver);
           if (lane == 0) {
-            over[4 * cb + quad] = mine;
+            reinterpret_cast<uint8_t*>(check + 2 * cb)[quad] = mine;
             mbar_arrive(B.soft + 2 * half + cb);
           }
         }
@@ -711,9 +736,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         };
         if (!move) {
           numerators();
-          wait(B.soft + 2 * half + cb, checks++ >> 1);
-          move = *reinterpret_cast<volatile uint32_t*>(over + 4 * cb) != 0;
+          wait1(B.soft + 2 * half + cb, nchecks++ >> 1);
+          const uint64_t c = *reinterpret_cast<volatile uint64_t*>(check + 2 * cb);
+          move = c != 0;
           if (move) {  // from the scores themselves
+            if (c >> 32) break;
             tmem_ld<RH>(sa, x);
 #pragma unroll
             for (int k = 0; k < RH; ++k) {
@@ -735,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
             const float w = warp_max_of<C>(y);
             if (lane < C) hr[quad * RH + c + lane] = w;
           }
-          soft_sync(half);
+          meet();
           if (st > 0) {  // the sums so far, once no product adds to them
-            wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
+            wait1(B.pv + ((i - 1) & 1), (i - 1) >> 1);
             fence_after();
           }
 #pragma unroll
@@ -801,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         open(s.r, u);
         --part;
       }
-      soft_sync(half);
+      meet();
       // ... its 1 / sum and its NaN blocks
       const float sum = (hsum[kl - k0] + hsum[RH + kl - k0]) + (hsum[2 * RH + kl - k0] + hsum[3 * RH + kl - k0]);
       const float inv_l = sum == 0.f ? 0.f : 1.f / sum;
@@ -814,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         for (int k = 1; k < RH; ++k) mk = lane == k ? m[k] : mk;
         if (quad == 0 && lane < RH && kl < rows) *reinterpret_cast<float2*>(pml + 2 * kl) = make_float2(mk, sum);
       }
-      wait(B.pv + ((i - 1) & 1), (i - 1) >> 1);
+      wait1(B.pv + ((i - 1) & 1), (i - 1) >> 1);
       fence_after();
       // the joining launch may line up now (from the start on, its CTAs had cost 2 us a call)
       if (u >= u1) mtail::pdl_trigger();
@@ -860,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     uint32_t i = 0;
     int r = r0;
     for (uint32_t u = u0; u < u1; qr.next()) {
+      if (dead()) break;
       const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
       r = s.r;
       const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first), row0 = starts[s.r];
@@ -896,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         if (lane == 0) mbar_arrive(B.q_full + qr.i);
       }
       for (int st = 0; st < steps; ++st, ++i, raw.next(), op.next()) {
-        wait(B.raw_full + raw.i, raw.ph);
+        wait1(B.raw_full + raw.i, raw.ph);
         const uint8_t* tp = sm + G::oRaw + raw.i * G::kStep + j * G::kTile;
         // keys: lane (g, c) holds 8 channels of each block of tokens g and g + 8
         uint32_t kw[D / 16], vw[D / 16];
@@ -941,6 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
         Info& inf = infos[i % kInfos];
         const bool plain = full && !__any_sync(~0u, nan != 0);
         if (!plain) {
+          if (dead()) break;
           // zero scales for tokens that no row sees, and for NaN scales, which the flags report
           const bool unseen = t0 < 0 || t0 + t > pmax;
           uint32_t fl = 0;
@@ -985,12 +1014,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     }
   }
 
-  if (*reinterpret_cast<volatile int*>(&s_dead)) {  // let the copies and products in flight end before their memory goes
+  if (*reinterpret_cast<volatile int*>(&s_dead)) {
+    if (lane == 0 && a.status) atomicOr(a.status, kStatusTimeout);
+    // let the copies and products in flight end before their memory goes
     const int64_t t0 = clock64();
     while (clock64() - t0 < 2000000) __nanosleep(1000);
   }
   fence_before();
   __syncthreads();
+  // (the joining launch must not follow a record that nobody wrote)
+  if (tid == 0 && *reinterpret_cast<volatile int*>(&s_dead)) recs[blockIdx.x].last = -1;
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 

@@ -841,6 +841,13 @@ extern "C" int moe_kv4_read(int32_t rows, int32_t kv_heads, int32_t head_dim, in
                   slots, status, stream);
 }
 
+static thread_local int g_kv4_stall = -1;
+
+extern "C" int moe_tail_debug_kv4_stall(int32_t barrier) {
+  g_kv4_stall = barrier;
+  return MOE_TAIL_OK;
+}
+
 static bool kv4_heads_ok(int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   return kv_heads >= 1 && kv_heads <= kv4::kMaxKvHeads && head_dim_ok(head_dim) && q_heads >= 1 &&
          q_heads % kv_heads == 0 && q_heads / kv_heads <= 256;
@@ -911,6 +918,8 @@ extern "C" int moe_kv4_attention(int32_t rows, int32_t reqs, int32_t q_heads, in
   a.out = (uint16_t*)out;
   a.ldo = ld_o;
   a.part = (float*)workspace;
+  a.stall = g_kv4_stall;
+  g_kv4_stall = -1;
   a.status = status;
   e = kv4::launch_kv4_attention(a, rn, (cudaStream_t)stream);
   return e == cudaSuccess ? MOE_TAIL_OK : cuda_fail(e);

@@ -33,6 +33,7 @@ def declare(lib):
     lib.moe_kv4_attention.argtypes = ([i32] * 6 + [i64, P, i64, P, P, i32, i64, P, P, f32, i32, i32,
                                                    i32, P, i64, P, ctypes.c_size_t, P, P])
     lib.moe_kv4_attention_workspace.argtypes = [i32] * 4
+    lib.moe_tail_debug_kv4_stall.argtypes = [i32]
     for name in ("moe_step_tables", "moe_qk_norm_rope", "moe_kv4_append", "moe_kv4_read",
                  "moe_kv4_attention"):
         getattr(lib, name).restype = ctypes.c_int
