@@ -54,9 +54,10 @@
 // must stay out of the steps: local memory shares what little L1 the 150..210 KB of shared memory leave,
 // and versions that spilled took 2.5 times as long.
 //
-// Tensor memory is taken whole (512 columns) before the previous kernel in the stream has ended.
-// That cannot lock up: no other tensor-memory kernel of this library fits beside a CTA of this one
-// (shared memory), and this one's CTAs hold theirs before they let the next kernel line up.
+// Tensor memory is taken whole (512 columns), once the kernels before this one in the stream have
+// ended: CTAs of this launch may be resident while a kernel of the caller's several launches back still
+// runs, and that one could otherwise wait for the columns that these hold while these wait for it.
+// The allocation runs beside the plan and costs nothing (1000 tokens 9.8 us either way).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -370,10 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
   if (warp == 2) {
     mtail::pdl_wait();
     int bits = 0;
@@ -397,6 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     if (warp == 3) *reinterpret_cast<uint4*>(sm + G::oSfI + lane * 16) = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
     fence_proxy();
     mtail::pdl_wait();
+    if (warp == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   fence_before();
   __syncthreads();
