@@ -54,7 +54,7 @@ extern "C" {
                                         skipped (its cache length cut to its table row by the
                                         attention) */
 #define MOE_KV4_STATUS_NO_PAGES 32   /* the free pages ran out: table entries and slots are -1 */
-#define MOE_KV4_STATUS_ROWS 64       /* the step has more rows than max_rows: the rest is cut */
+#define MOE_KV4_STATUS_ROWS 64       /* the step has more rows than max_rows: it was cut to these */
 #define MOE_KV4_STATUS_BAD_SLOT 128  /* a slot past the cache: the row was skipped */
 #define MOE_KV4_STATUS_BAD_PAGE 256  /* a page number outside the cache: its tokens are masked */
 
@@ -63,9 +63,11 @@ extern "C" {
 #define MOE_KV4_MAX_PAGE 1024
 
 /* Tables of one step, from lengths: request r has cached_lens[r] tokens in the cache and
- * new_lens[r] rows in this step (0: none).
- *   row_starts[r]  = sum of new_lens[0 .. r-1], row_starts[reqs] = all rows T
- *   kv_lens[r]     = cached_lens[r] + new_lens[r]
+ * new_lens[r] rows in this step (0: none).  Where all rows are more than max_rows (status ROWS),
+ * the step is cut to its first max_rows: new[r] below is what is left of new_lens[r], so that the
+ * tables are those of a step with these fewer rows, and the caller may send the others in the next.
+ *   row_starts[r]  = sum of new[0 .. r-1], row_starts[reqs] = all rows T
+ *   kv_lens[r]     = cached_lens[r] + new[r]
  *   row i of request r (row_starts[r] <= i < row_starts[r+1]):
  *     positions[i] = cached_lens[r] + i - row_starts[r]
  *     slots[i]     = block_table[r][positions[i] / page_size] * page_size

@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
     const uint32_t r1 = __shfl_up_sync(~0u, wr, o), p1 = __shfl_up_sync(~0u, wp, o);
     if (lane >= o) wr = add_sat(wr, r1), wp = add_sat(wp, p1);
   }
-  const uint32_t all_rows = __shfl_sync(~0u, wr, 31), all_pages = __shfl_sync(~0u, wp, 31);
+  const uint32_t all_rows = __shfl_sync(~0u, wr, 31);
+  uint32_t all_pages = __shfl_sync(~0u, wp, 31);
   const uint32_t r0 = __shfl_sync(~0u, wr, max(warp - 1, 0)), p0 = __shfl_sync(~0u, wp, max(warp - 1, 0));
   if (warp) r = add_sat(r, r0), p = add_sat(p, p0);
   if (tid < R) {
@@ -130,6 +131,25 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
   }
   if (tid == 0) s_row[0] = s_page[0] = 0;
   __syncthreads();
+  if ((int)all_rows > a.max_rows) {  // (the same in every thread)
+    // a cut step: lengths and pages go by the rows that are kept
+    if (tid < R) n = s_row[tid + 1] - s_row[tid], want = n ? pages(c + n) : have;
+    p = want - have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t p1 = __shfl_up_sync(~0u, p, o);
+      if (lane >= o) p = add_sat(p, p1);
+    }
+    if (lane == 31) s_wp[warp] = p;
+    __syncthreads();
+    all_pages = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w == warp) p = add_sat(p, all_pages);
+      all_pages = add_sat(all_pages, s_wp[w]);
+    }
+    if (tid < R) s_page[tid + 1] = (int)p;
+    __syncthreads();
+  }
 
   if (blockIdx.x == 0) {
     if (tid < R) {
@@ -145,7 +165,7 @@ __global__ void __launch_bounds__(kMaxReqs) k_step_tables(const TablesArgs a) {
     report(a.status, bits);
   }
 
-  const int step = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + tid;  // (max_rows is at most 2^20)
+  const int step = gridDim.x * blockDim.x, at = blockIdx.x * blockDim.x + tid;  // (max_rows is at most 2^24)
   const int T = s_row[R];
   for (int i = at; i < a.max_rows; i += step) {
     int pos = 0;

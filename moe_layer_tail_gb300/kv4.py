@@ -160,7 +160,9 @@ def step_tables(cached_lens, new_lens, free_pages, block_table, page_size: int, 
     """Block tables, row starts, positions and slots of one step from the requests' lengths
     (moe_step_tables).  cached_lens, new_lens int32 [reqs]; free_pages int32 [n] or None;
     block_table int32 [reqs, width], filled in place; row_starts int32 [reqs + 1], kv_lens int32
-    [reqs], positions int32 and slots int64 [max_rows], pages_used int32 [1]: written."""
+    [reqs], positions int32 and slots int64 [max_rows], pages_used int32 [1]: written.  A step of
+    more than max_rows rows is cut to its first ones (KV4_STATUS_ROWS): kv_lens and pages_used
+    count the rows that are left."""
     w = "step_tables"
     torch, lib, dev = _begin(w, cached_lens)
     i32 = torch.int32

@@ -12,7 +12,19 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
 
 
+# A test that holds a value which contradicts the interface: it stays as it is and has to fail.
+# step_tables of a cut step (kv4_attn.h, status ROWS) gave kv_lens of 40 to a request of which 16 rows
+# were left, so that the attention took its first row, at positions[] 0, for the one at 24.
+# test_gpu_kv4_cut_step.py has the values that fit together.
+CONTRADICTED = {"test_gpu_kv4.py::test_step_tables_reports[rows]":
+                "kv_lens and pages count rows that a cut step does not have"}
+
+
 def pytest_collection_modifyitems(config, items):
+    for item in items:
+        for name, why in CONTRADICTED.items():
+            if item.nodeid.endswith(name):
+                item.add_marker(pytest.mark.xfail(reason=why, strict=True, raises=AssertionError))
     try:
         import torch
         has_gpu = torch.cuda.is_available()
