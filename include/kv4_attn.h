@@ -48,7 +48,8 @@
 extern "C" {
 #endif
 
-/* Bits of a *status word (MOE_TAIL_STATUS_TIMEOUT may join them). */
+/* Bits of a *status word.  MOE_TAIL_STATUS_TIMEOUT may join them: a hand-over inside the attention did
+ * not come in some 0.1 s, and the rows that were to come of it are NaN. */
 #define MOE_KV4_STATUS_BAD_LENGTH 16 /* a negative length, one past its table row, row starts
                                         that descend or pass the call's rows; the request is
                                         skipped (its cache length cut to its table row by the

@@ -50,9 +50,9 @@
 // 1 issues K' and S, 14 V' and O (an elected thread each: a divergent issuer costs 45 cycles an
 // instruction, an elected one 9 at these sizes); 2..5 and 15..18 are the softmax and the output of
 // the lower and the upper half of the rows.  They hand over through mbarriers; every wait is bounded
-// and reports MOE_TAIL_STATUS_TIMEOUT; a CTA in which one has given up ends without its results.  Spills
-// must stay out of the steps: local memory shares what little L1 the 150..210 KB of shared memory leave,
-// and versions that spilled took 2.5 times as long.
+// and reports MOE_TAIL_STATUS_TIMEOUT; a CTA in which one has given up leaves NaN in the rows that it
+// had a part of.  Spills must stay out of the steps: local memory shares what little L1 the 150..210 KB
+// of shared memory leave, and versions that spilled took 2.5 times as long.
 //
 // Tensor memory is taken whole (512 columns), once the kernels before this one in the stream have
 // ended: CTAs of this launch may be resident while a kernel of the caller's several launches back still
@@ -315,6 +315,36 @@ struct JoinRec {
   int rows;   // rows of the item
   int pad[3];
 };
+
+// What a CTA whose waits gave up leaves of its range, whatever it had written of it: NaN in the rows of its
+// whole items, and parts that make the rows of the others NaN when they are joined.
+template <int D, int RN>
+__device__ __forceinline__ void forsake(const AttnArgs& a, const uint32_t* pre, const int* lens, const int* starts,
+                                     uint32_t u0, uint32_t u1, uint32_t per) {
+  JoinRec rec = {};
+  rec.last = -1;
+  int r = find_req(pre, a.reqs, u0);
+  for (uint32_t u = u0; u < u1;) {
+    const Seg s = open_seg(a, RN, pre, lens, starts, r, u, u1);
+    r = s.r;
+    const int first = s.j * RN, nrow = min(RN, s.q.nq * a.G - first);
+    const bool whole = s.k0 == 0 && s.k1 == s.q.n;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (s.k0 == 0 ? 1 : 0);
+    float2* ml = reinterpret_cast<float2*>(a.part + 2 * (int64_t)a.ctas * RN * D) + slot * RN;
+    for (int i = threadIdx.x; i < nrow * D; i += kThreads) {
+      const int k = i / D, rho = first + k, tk = rho / a.G;
+      if (whole) a.out[(starts[s.r] + tk) * a.ldo + (int64_t)(s.h * a.G + rho - tk * a.G) * D + i % D] = 0x7FC0;
+      else if (i % D == 0) ml[k] = make_float2(0.f, __uint_as_float(0x7FC00000u));
+    }
+    u += s.places;
+    if (u >= u1) {
+      if (s.k0 == 0 && !whole) rec.last = (int)((s.item + (uint32_t)(s.q.n + kItemTiles) - 1) / per);
+      rec.row0 = starts[s.r], rec.first = first, rec.head = s.h, rec.rows = nrow;
+    }
+  }
+  if (threadIdx.x == 0)
+    reinterpret_cast<JoinRec*>(a.part + 2 * (int64_t)a.ctas * RN * (D + 2))[blockIdx.x] = rec;
+}
 
 template <int D, int RN>
 __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant__ AttnArgs a) {
@@ -1023,8 +1053,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   }
   fence_before();
   __syncthreads();
-  // (the joining launch must not follow a record that nobody wrote)
-  if (tid == 0 && *reinterpret_cast<volatile int*>(&s_dead)) recs[blockIdx.x].last = -1;
+  if (*reinterpret_cast<volatile int*>(&s_dead)) {
+    const volatile uint32_t* range = s_range;  // (read again: kept in registers it cost the steps spills)
+    forsake<D, RN>(a, pre, lens, starts, range[0], range[1], range[2]);
+  }
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 

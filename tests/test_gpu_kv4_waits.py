@@ -84,6 +84,22 @@ def test_a_hand_over_that_never_comes_ends_the_call(D, G):
     assert len(seen) == used and n not in seen
 
 
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 16), (256, 4), (256, 32)])
+def test_rows_that_were_given_up_are_nan(D, G):
+    # without a status word: each head of a row is what it always is, or NaN throughout
+    n, _ = barriers(D)
+    for b in batches(D, G):
+        clean, _ = b.run()
+        nan = np.zeros(clean.shape[:2], bool)
+        for stall in (0, n // 2, n - 10, n - 1):
+            out, _ = b.run(stall, report=False)
+            gone = (out & 0x7FFF) > 0x7F80
+            assert np.array_equal(gone.all(-1), gone.any(-1))
+            assert np.array_equal(out[~gone], clean[~gone])
+            nan |= gone.any(-1)
+        assert 0 < nan.sum() < nan.size
+
+
 def test_the_order_holds_for_one_call_and_can_be_taken_back():
     b = next(batches(64, 8))
     clean, _ = b.run()
