@@ -154,7 +154,7 @@ int moe_kv4_read(int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t page_
  * scale finite and > 0, window >= 0, sinks >= 0 (ignored when window == 0), max_new >= 1; q, out,
  * cache 16-byte aligned, strides multiples of 8 (at least q_heads * D).  A call whose requests
  * would read more than 2^31 - 1 tiles (of 16 tokens, once for each kv head and up to 32 rows, and
- * 36 more for each of those) sets BAD_LENGTH and computes nothing. */
+ * 36 more for each of those) sets BAD_LENGTH and computes nothing: its rows are NaN. */
 int moe_kv4_attention(int32_t rows, int32_t reqs, int32_t q_heads, int32_t kv_heads,
                       int32_t head_dim, int32_t page_size, int64_t n_pages, const void* q,
                       int64_t ld_q, const void* cache, const int32_t* block_table,

@@ -307,8 +307,9 @@ struct Bars {
 };
 
 // The record that tells the joining launch which item crosses the end of a range.
+constexpr int kRefused = -2;
 struct JoinRec {
-  int last;   // the last range of the item, negative: none crosses
+  int last;   // the last range of the item, negative: none crosses; kRefused: the call is too large
   int row0;   // first query row of its request
   int first;  // the item's first row among the request's (row, head) pairs
   int head;   // kv head
@@ -407,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
     const uint64_t total64 = plan(a, RN, plan_load(a, lane), pre, lens, starts, &bits);
     if (total64 > 0x7FFFFFFFull) bits |= kStatusBadLength;
     if (blockIdx.x == 0 && bits && a.status) atomicOr(a.status, bits);
-    const uint32_t total = total64 > 0x7FFFFFFFull ? 0u : (uint32_t)total64, per = range_tiles(total, a.ctas);
+    const uint32_t total = total64 > 0x7FFFFFFFull ? 0u : (uint32_t)total64;
+    const uint32_t per = total64 > 0x7FFFFFFFull ? 0u : range_tiles(total, a.ctas);
     const uint32_t u0 = (uint32_t)min((uint64_t)blockIdx.x * per, (uint64_t)total);
     __syncwarp();
     const uint32_t u1 = range_end(a, RN, pre, lens, starts, u0, min(total, u0 + per));
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   fence_after();
   const uint32_t u0 = s_range[0], u1 = s_range[1], per = s_range[2];
   const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
-  if (u0 == u1 && tid == 0) recs[blockIdx.x].last = -1;
+  if (u0 == u1 && tid == 0) recs[blockIdx.x].last = per ? -1 : kRefused;
 
   // A wait gave up, here or elsewhere in the CTA (of each lane: a warp asks for it by a vote).  From then
   // on a wait takes one sleep at most and every role leaves its loops where it next asks; the
@@ -1074,6 +1076,16 @@ __global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ AttnAr
   mtail::pdl_wait();
   const JoinRec rec = reinterpret_cast<const JoinRec*>(a.part + 2 * (int64_t)a.ctas * RN * (D + 2))[blockIdx.x];
   const int i = blockIdx.y * 4 + warp;
+  if (rec.last == kRefused) {  // NaN for every row of a request
+    const int w = (blockIdx.x * gridDim.y + blockIdx.y) * 4 + warp, width = a.heads * a.G * D;
+    for (int r = 0; r < a.reqs; ++r) {
+      int bits = 0;
+      const int rs = a.row_starts[r], n = req_of(a, RN, a.kv_lens[r], rs, a.row_starts[r + 1], &bits).nq;
+      for (int t = w; t < n; t += gridDim.x * gridDim.y * 4)
+        for (int c = lane; c < width; c += 32) a.out[(int64_t)(rs + t) * a.ldo + c] = 0x7FC0;
+    }
+    return;
+  }
   if (rec.last < 0 || i >= rec.rows) return;
   const int c0 = blockIdx.x, n = rec.last - c0 + 1;
   // part k's slot: the item begins in the second one of its first range, then takes the first ones

@@ -263,7 +263,9 @@ def kv4_attention(q, cache, block_table, row_starts, kv_lens, out, scale: float 
     otherwise the last `window` tokens and the first `sinks`.  workspace: uint8, at least
     kv4_attention_workspace bytes, not shared with a call that may run at the same time (two
     captured graphs replayed in different streams need two); None takes one from PyTorch's
-    allocator for this call."""
+    allocator for this call.  A call of more than 2^31 - 1 tiles of 16 tokens (counted for each kv
+    head and 32 rows: some 90000 rows of a prompt with 16 query heads to each of 8 kv heads) gives
+    NaN and KV4_STATUS_BAD_LENGTH: cut the prompt into several calls."""
     w = "kv4_attention"
     torch, lib, dev = _begin(w, q)
     i32, bf = torch.int32, torch.bfloat16
