@@ -138,7 +138,8 @@ int moe_kv4_read(int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t page_
  *   q bf16 [rows, q_heads, D], out likewise, row strides ld_q, ld_o in elements; out must not
  *   overlap an input
  *   block_table int32 [reqs] rows of table_width entries, table_stride apart
- * Rows that no request has (from row_starts[reqs] on) are left as they were.  `max_new` is the
+ * Rows that no request has (from row_starts[reqs] on) are left as they were; a row that two requests
+ * have, which takes row starts that descend between them (BAD_LENGTH), holds what either gives it.  `max_new` is the
  * caller's estimate of the largest number of rows of a request; it steers how the work is cut
  * and does not change what is computed.  `workspace` (16-byte aligned, exclusive to the call
  * until it has completed) holds workspace_bytes >= moe_kv4_attention_workspace(..) with the same
