@@ -94,9 +94,9 @@ struct AttnArgs {
   int32_t* status;
 };
 // Query rows of one work item for calls with up to `max_new` rows of a request.
-int attn_rows_per_item(int D, int G, int max_new);
+int attn_rows_per_item(int G, int max_new);
 // CTAs of the attention launch on the current device (0 on a CUDA error, left in *err).
-int attn_ctas(int D, int rn, cudaError_t* err);
+int attn_ctas(cudaError_t* err);
 size_t attn_workspace_bytes(int D, int rn, int ctas);
 cudaError_t launch_kv4_attention(const AttnArgs& a, int rn, cudaStream_t st);
 

@@ -1193,12 +1193,12 @@ cudaError_t dispatch(int D, int rn, F&& f) {
 
 }  // namespace
 
-int attn_rows_per_item(int D, int G, int max_new) {
+int attn_rows_per_item(int G, int max_new) {
   const int64_t rows = (int64_t)G * max_new;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 
-int attn_ctas(int D, int rn, cudaError_t* err) {
+int attn_ctas(cudaError_t* err) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -857,9 +857,9 @@ extern "C" int64_t moe_kv4_attention_workspace(int32_t q_heads, int32_t kv_heads
                                                int32_t head_dim, int32_t max_new) {
   if (max_new < 1) return MOE_TAIL_ERR_INVALID_ARG;
   if (!kv4_heads_ok(q_heads, kv_heads, head_dim)) return MOE_TAIL_ERR_UNSUPPORTED;
-  const int rn = kv4::attn_rows_per_item(head_dim, q_heads / kv_heads, max_new);
+  const int rn = kv4::attn_rows_per_item(q_heads / kv_heads, max_new);
   cudaError_t e = cudaSuccess;
-  const int ctas = kv4::attn_ctas(head_dim, rn, &e);
+  const int ctas = kv4::attn_ctas(&e);
   if (e != cudaSuccess) return cuda_fail(e);
   return (int64_t)kv4::attn_workspace_bytes(head_dim, rn, ctas);
 }
@@ -889,9 +889,9 @@ extern "C" int moe_kv4_attention(int32_t rows, int32_t reqs, int32_t q_heads, in
   kv4::AttnArgs a;
   a.G = q_heads / kv_heads;
   a.D = head_dim;
-  const int rn = kv4::attn_rows_per_item(head_dim, a.G, max_new);
+  const int rn = kv4::attn_rows_per_item(a.G, max_new);
   cudaError_t e = cudaSuccess;
-  a.ctas = kv4::attn_ctas(head_dim, rn, &e);
+  a.ctas = kv4::attn_ctas(&e);
   if (e != cudaSuccess) return cuda_fail(e);
   if (workspace_bytes < kv4::attn_workspace_bytes(head_dim, rn, a.ctas))
     return MOE_TAIL_ERR_INVALID_ARG;

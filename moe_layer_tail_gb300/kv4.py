@@ -13,6 +13,9 @@ checked here, everything runs in the library's CUDA kernels on the tensors' devi
 
 `status` (optional everywhere): an int32 CUDA tensor of one element into which the kernels OR
 KV4_STATUS_* bits; the caller zeroes it.
+`stream` (optional everywhere): the torch.cuda.Stream to launch in, in place of the current one.
+PyTorch's allocator does not learn of it: the caller keeps the tensors alive until the work there
+has passed them (or calls record_stream on them).
 """
 import ctypes
 
@@ -263,7 +266,8 @@ def kv4_attention(q, cache, block_table, row_starts, kv_lens, out, scale: float 
     otherwise the last `window` tokens and the first `sinks`.  workspace: uint8, at least
     kv4_attention_workspace bytes, not shared with a call that may run at the same time (two
     captured graphs replayed in different streams need two); None takes one from PyTorch's
-    allocator for this call.  A call of more than 2^31 - 1 tiles of 16 tokens (counted for each kv
+    allocator for this call, which a graph captured by torch.cuda.graph keeps; a capture begun in
+    any other way must be given one, since nothing would keep that memory for its replays.  A call of more than 2^31 - 1 tiles of 16 tokens (counted for each kv
     head and 32 rows: some 90000 rows of a prompt with 16 query heads to each of 8 kv heads) gives
     NaN and KV4_STATUS_BAD_LENGTH: cut the prompt into several calls."""
     w = "kv4_attention"
