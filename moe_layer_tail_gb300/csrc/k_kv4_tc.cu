@@ -28,21 +28,22 @@
 // Conversions on the CUDA cores into mma.sync had taken 490 warp instructions per tile and stayed
 // at 2.5 TB/s.
 //
-// What bounds it (524287 tokens, 8 kv heads of 128, 16 query heads each: 570 MB in 135 us, 4.2 TB/s,
-// 0.62 of the measured copy rate): not the tensor cores (about 550 cycles of products a step), not
+// What bounds it (524287 tokens, 8 kv heads of 128, 16 query heads each: 570 MB in 139 us, 4.1 TB/s,
+// 0.61 of the measured copy rate): not the tensor cores (about 550 cycles of products a step), not
 // the memory (740 cycles for a step's 17 KB) but two chains of hand-overs of about 1100 cycles a
 // step each, K' -> S -> K' of the next step (each product is seen complete about 300 cycles after
 // its last instruction has issued, and K' has room for one step only) and S -> P -> S of the
-// softmax.  Tensor memory is full at D 128 (K' 128 columns, V' 2 x 128, S, O, scales of 512), so
-// neither can run further ahead.  Tried and slower at this size: K' in a ring of three blocks of 64
+// softmax.  Tensor memory has no room for K' twice at D 128 (K' 128 columns, V' 2 x 128, S twice, O and
+// the scales are 456 of 512 with up to 16 rows an item, 504 with 32), so neither can run further ahead.
+// Tried and slower at this size (against 135 us at the time): K' in a ring of three blocks of 64
 // channels with a warp of its own (163 us: six runs of products a step instead of four, and each
 // costs the pipe some 150 cycles beside its products); both dequantisations in one run (160); a warp
 // of its own for V' (141: its products get in front of the scores' in the pipe), V' before the output
 // product (140); V' and K' in halves (234); waits that poll (185; a dozen polling warps take the
 // shared-memory pipe from the others); one group of four softmax warps (190).  D 64 has the same
 // chains for half the bytes (K' twice there changed nothing); D 256 twice the products for its two
-// halves of channels: four rows of eight requests of up to 16384 tokens, 64 rows a kv head, take 71
-// us in two items of 32 rows and took 103 in four of 16.
+// halves of channels: four rows of eight requests of up to 16384 tokens, 64 rows a kv head, take 73
+// us in two items of 32 rows (71 at the time, and 103 in four of 16).
 //
 // Warps: 0 looks up pages and copies tiles (bulk copies into a ring, 32 look-ups at a time);
 // 6..13 (one per tile of a step) bring a tile's bytes, which the cache holds in the order of
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_attn(const __grid_constant_
   // softmax and the layout ask in what they read anyway, which warp 0 marks as it leaves.  What a warp
   // still does then may differ from the others', so none waits for another but at these barriers, and
   // all reach the kernel's last.  (Small code: a variable that lives through the steps of all
-  // roles, or a longer way out of each wait, cost 4 to 25 % of a long call; this 2 %.)
+  // roles, or a longer way out of each wait, cost 4 to 25 % of a long call; this 2 to 3 %.)
   bool gone = false;
   auto wait = [&](uint64_t* b, uint32_t parity) {
     if (mbar_test(b, parity & 1)) return;  // (quicker than the waiting form where it has completed)
