@@ -58,7 +58,8 @@
 // Tensor memory is taken whole (512 columns), once the kernels before this one in the stream have
 // ended: CTAs of this launch may be resident while a kernel of the caller's several launches back still
 // runs, and that one could otherwise wait for the columns that these hold while these wait for it.
-// The allocation runs beside the plan and costs nothing (1000 tokens 9.8 us either way).
+// The allocation runs beside the plan and costs nothing (1000 and 524287 tokens took the same before and
+// behind).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
